@@ -7,7 +7,12 @@
  *   - the BCJR forward-backward relaxation at a temperature (soft codeword)
  *     and its vector-Jacobian product,
  *   - packing state walks into bitstreams and the sliding-window decode of
- *     those streams to fp16 weights.
+ *     those streams to fp16 weights;
+ * and what a decoded matrix is used for next:
+ *   - its decode to int8, row-wise int8 quantisation of activations and the
+ *     int8 matrix product with scales for each token and channel,
+ *   - the gated feed-forward block act(x Wg^T) * (x Wu^T) on 16-bit weights
+ *     with its gradients, and on int8 weights.
  *
  * Sources:
  *   [QTIP]  blog post "QTIP: Trellis-Coded Quantization Puts 2-Bit LLM Weights
@@ -301,6 +306,127 @@ TCQ_API tcq_status_t tcq_decode_gemv(const tcq_trellis_t *trellis, const uint32_
  * ------------------------------------------------------------------------ */
 TCQ_API tcq_status_t tcq_rht(const float *W, int64_t rows, int64_t cols, const float *sign_rows,
                              const float *sign_cols, float *out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Matrix products on decoded weights.
+ *
+ * Conventions of the calls below, beside the common ones: element types are
+ * TCQ_F16, TCQ_BF16 and TCQ_F32; a weight matrix is [out][in] row-major, so
+ * a product is x W^T; n_tok counts tokens (rows of x).  n_tok = 0 is an empty
+ * batch (weight gradients are then zero); a zero `rows`, `cols`, `n_out` or
+ * `n_in` is an invalid argument.  Sizes are at most 2^30 - 1 each
+ * (TCQ_ERR_UNSUPPORTED beyond), n_in of an int8 product at most 131,071 (its
+ * 32-bit sums cannot overflow).  Any other size is taken; n_in a multiple of
+ * 16 bytes (8 elements of 16 bits, 16 of int8) spares a copy of the operands
+ * into the workspace, n_out a multiple of 16 elements spares narrow stores.
+ * Outputs may not overlap inputs.  `ws` is a device workspace of at least the
+ * matching *_workspace_size() bytes, 256-byte aligned (a size of 0 allows
+ * NULL); nothing in it is kept between calls.
+ * A value that is not finite spreads as in the formulas: an infinity or NaN
+ * of x reaches the outputs of its token alone (and the weight gradients),
+ * one of a weight row the outputs of its channel (and grad_x).
+ * Results do not depend on what else runs and repeat bit for bit.
+ * ------------------------------------------------------------------------ */
+enum { TCQ_F16 = 0, TCQ_BF16 = 1, TCQ_F32 = 2 };
+
+/* Activations: v / (1 + e^-v); v Phi(v) (normal distribution function); its
+ * tanh form v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2; max(v, 0). */
+enum { TCQ_ACT_SILU = 0, TCQ_ACT_GELU = 1, TCQ_ACT_GELU_TANH = 2, TCQ_ACT_RELU = 3 };
+
+/* ------------------------------------------------------------------------
+ * Row-wise symmetric int8 quantisation:
+ *   scale[m] = max_k |x[m][k]| / 127, rounded once to fp32,
+ *   q[m][k]  = x[m][k] / scale[m] rounded to the nearest integer, ties to the
+ *              even one (decided exactly, not on a rounded quotient).
+ * A row of zeros (or one so small that its scale rounds to zero) gives scale
+ * 0 and q 0; a row that holds an infinity or a NaN gives scale NaN and q 0, so
+ * that a product with it shows the NaN.
+ *   x [rows][cols] of `dtype` (input), q [rows][cols] int8, scale [rows] fp32
+ *   (outputs).  rows = 0 is an empty batch.
+ * ------------------------------------------------------------------------ */
+TCQ_API tcq_status_t tcq_quantize_int8(const void *x, int dtype, int64_t rows, int64_t cols,
+                                       int8_t *q, float *scale, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Sliding-window decode to int8: the streams, layouts and arguments of
+ * tcq_decode, but every weight is written as
+ *   q = (bytesum - 510) / 4 rounded to the nearest integer, ties to even,
+ * so the 1MAD code is q * 4 / 147.8 to within half a step of 4 / 147.8 (a
+ * mean squared error of 7e-5 of the unit-variance code, against about 0.07
+ * that the 2-bit quantisation leaves).  |q| <= 121 for every state at L = 8,
+ * 12 and 16.  Multiply a channel's scale by 4 / 147.8 for tcq_int8_matmul.
+ * ------------------------------------------------------------------------ */
+TCQ_API tcq_status_t tcq_decode_int8(const tcq_trellis_t *trellis, const uint32_t *bits,
+                                     int64_t n_seq, int layout, int out_layout, int64_t rows,
+                                     int64_t cols, int8_t *out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Matrix product of int8 values with a scale for each token and channel:
+ *   out[m][n] = a_scale[m] w_scale[n] sum_k a[m][k] w[n][k] + bias[n],
+ * the sum exact in 32-bit integers, the rest in fp32 (sum, times a_scale,
+ * times w_scale, plus bias, in this order), rounded once to out_dtype.
+ *   a [n_tok][n_in] int8, a_scale [n_tok] fp32, w [n_out][n_in] int8, w_scale
+ *   [n_out] fp32, bias [n_out] fp32 or NULL (inputs); out [n_tok][n_out] of
+ *   out_dtype (output).
+ * ------------------------------------------------------------------------ */
+TCQ_API size_t tcq_int8_matmul_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in);
+
+TCQ_API tcq_status_t tcq_int8_matmul(const int8_t *a, const float *a_scale, const int8_t *w,
+                                     const float *w_scale, const float *bias, int64_t n_tok,
+                                     int64_t n_out, int64_t n_in, void *out, int out_dtype,
+                                     void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Gated feed-forward block, the two projections, the activation and the
+ * product in one kernel:
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u,
+ * sums and activation in fp32, h rounded once.
+ *   x [n_tok][n_in], w_gate, w_up [n_out][n_in] of `dtype` (TCQ_F16 or
+ *   TCQ_BF16; inputs); h [n_tok][n_out] of `dtype` (output); gate, up
+ *   [n_tok][n_out] fp32: g and u for tcq_gated_ffn_backward (outputs, both or
+ *   neither NULL).
+ * ------------------------------------------------------------------------ */
+TCQ_API size_t tcq_gated_ffn_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in);
+
+TCQ_API tcq_status_t tcq_gated_ffn(const void *x, const void *w_gate, const void *w_up, int dtype,
+                                   int64_t n_tok, int64_t n_out, int64_t n_in, int act, void *h,
+                                   float *gate, float *up, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Gradients of the gated feed-forward block:
+ *   dg = grad_h u act'(g),  du = grad_h act(g)   (fp32, rounded to `dtype`),
+ *   grad_x = dg Wg + du Wu,  grad_w_gate = dg^T x,  grad_w_up = du^T x,
+ * sums in fp32, each result rounded once.  dg and du are operands of a 16-bit
+ * matrix product, hence their rounding; at TCQ_F16 entries below 6e-5 lose
+ * digits, so scale the loss as usual for fp16.  The slope of TCQ_ACT_RELU at 0
+ * is 0.
+ *   x, w_gate, w_up, grad_h of `dtype`, gate, up fp32 as tcq_gated_ffn wrote
+ *   them (inputs); grad_x [n_tok][n_in], grad_w_gate, grad_w_up [n_out][n_in]
+ *   of `dtype` (outputs, each may be NULL: it is then not computed).
+ * ------------------------------------------------------------------------ */
+TCQ_API size_t tcq_gated_ffn_backward_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in);
+
+TCQ_API tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up,
+                                            const float *gate, const float *up, const void *grad_h,
+                                            int dtype, int64_t n_tok, int64_t n_out, int64_t n_in,
+                                            int act, void *grad_x, void *grad_w_gate,
+                                            void *grad_w_up, void *ws, size_t ws_bytes,
+                                            void *stream);
+
+/* ------------------------------------------------------------------------
+ * Gated feed-forward block on int8 operands:
+ *   g = a_scale[m] w_gate_scale[n] sum_k a[m][k] w_gate[n][k], u alike,
+ *   h = act(g) * u,
+ * sums exact in 32-bit integers, the rest in fp32, rounded once.
+ *   Shapes and types as in tcq_int8_matmul and tcq_gated_ffn.
+ * ------------------------------------------------------------------------ */
+TCQ_API size_t tcq_int8_gated_ffn_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in);
+
+TCQ_API tcq_status_t tcq_int8_gated_ffn(const int8_t *a, const float *a_scale, const int8_t *w_gate,
+                                        const float *w_gate_scale, const int8_t *w_up,
+                                        const float *w_up_scale, int64_t n_tok, int64_t n_out,
+                                        int64_t n_in, int act, void *h, int out_dtype, void *ws,
+                                        size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

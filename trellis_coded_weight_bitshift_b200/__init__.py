@@ -17,6 +17,14 @@ computed" / "Tail-biting is worth its complexity"; BCJR-QAT abstract):
   pack_states(states, L, layout)         -> bits uint32 [n, words]
   decode(bits, L, T, layout, ...)        -> fp16 weights
   rht(W, sign_rows, sign_cols)           -> random-sign Hadamard rotation of W
+Products on decoded weights:
+  quantize_int8(x)                       -> (int8 rows, fp32 scale a row)
+  decode_int8(bits, L, T, layout, ...)   -> int8 weights (scale DECODE_INT8_SCALE)
+  int8_matmul(a, a_scale, w, w_scale)    -> a w^T with token and channel scales
+  gated_ffn(x, w_gate, w_up, act)        -> act(x w_gate^T) * (x w_up^T)
+  gated_ffn_backward(...)                -> its three gradients
+  GatedFfn.apply(x, w_gate, w_up, act)   -> the block under autograd
+  int8_gated_ffn(a, a_scale, ...)        -> the block on int8 tokens and weights
 """
 from __future__ import annotations
 
@@ -25,15 +33,24 @@ import ctypes
 import torch
 
 from . import _abi
-from ._abi import (FREE_START, OUT_SEQ, OUT_TILE16, TAILBITING, TcqError, check, lib,
-                   status_string, trellis)
+from ._abi import (ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SILU, FREE_START, OUT_SEQ, OUT_TILE16,
+                   TAILBITING, TcqError, check, lib, status_string, trellis)
 
 __all__ = [
     "viterbi_encode", "viterbi_encode_tailbiting", "bcjr_soft", "bcjr_soft_and_grad", "bcjr_soft_backward", "BcjrSoft", "pack_states", "decode",
     "stream_words", "viterbi_workspace_size", "bcjr_workspace_size", "TcqError", "rht",
     "decode_gemv",
     "TAILBITING", "FREE_START", "OUT_SEQ", "OUT_TILE16", "lib", "status_string",
+    "quantize_int8", "decode_int8", "int8_matmul", "gated_ffn", "gated_ffn_backward", "GatedFfn",
+    "int8_gated_ffn", "DECODE_INT8_SCALE", "int8_matmul_workspace_size", "gated_ffn_workspace_size",
+    "gated_ffn_backward_workspace_size", "int8_gated_ffn_workspace_size",
+    "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "ACT_RELU",
 ]
+
+# one step of decode_int8 in units of the 1MAD code: (bytesum - 510) / 147.8 = 4 q / 147.8
+DECODE_INT8_SCALE = 4 / 147.8
+
+_DTYPE = {torch.float16: _abi.F16, torch.bfloat16: _abi.BF16, torch.float32: _abi.F32}
 
 
 def _require_cuda(*tensors: "torch.Tensor | None") -> None:
@@ -311,3 +328,202 @@ def decode_gemv(bits: torch.Tensor, x: torch.Tensor, rows: int, cols: int, L: in
     check(lib().tcq_decode_gemv(ctypes.byref(tr), _ptr(bits), int(layout), int(rows), int(cols),
                                 _ptr(x), _ptr(y), _stream()), "tcq_decode_gemv")
     return y
+
+
+def int8_matmul_workspace_size(n_tok: int, n_out: int, n_in: int) -> int:
+    return int(lib().tcq_int8_matmul_workspace_size(int(n_tok), int(n_out), int(n_in)))
+
+
+def gated_ffn_workspace_size(n_tok: int, n_out: int, n_in: int) -> int:
+    return int(lib().tcq_gated_ffn_workspace_size(int(n_tok), int(n_out), int(n_in)))
+
+
+def gated_ffn_backward_workspace_size(n_tok: int, n_out: int, n_in: int) -> int:
+    return int(lib().tcq_gated_ffn_backward_workspace_size(int(n_tok), int(n_out), int(n_in)))
+
+
+def int8_gated_ffn_workspace_size(n_tok: int, n_out: int, n_in: int) -> int:
+    return int(lib().tcq_int8_gated_ffn_workspace_size(int(n_tok), int(n_out), int(n_in)))
+
+
+def quantize_int8(x: torch.Tensor):
+    """Row-wise symmetric int8 quantisation of ``x`` [rows, cols] (fp16, bf16
+    or fp32); returns (q int8 [rows, cols], scale fp32 [rows]) with x ~ q *
+    scale: scale = max|row| / 127, q = x / scale rounded to nearest, ties to
+    even.  A zero row gives scale 0, a row with an infinity or NaN scale NaN."""
+    _require_cuda(x)
+    if x.dim() != 2 or x.dtype not in _DTYPE:
+        raise ValueError("x must be a 2-D float16, bfloat16 or float32 tensor")
+    rows, cols = x.shape
+    q = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    check(lib().tcq_quantize_int8(_ptr(x), _DTYPE[x.dtype], rows, cols, _ptr(q), _ptr(scale),
+                                  _stream()), "tcq_quantize_int8")
+    return q, scale
+
+
+def decode_int8(bits: torch.Tensor, L: int, seq_len: int = 256, layout: int = TAILBITING,
+                out_layout: int = OUT_SEQ, rows: int = 0, cols: int = 0,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """Decode bitstreams as ``decode`` does, but to int8: the code is
+    DECODE_INT8_SCALE times the result to within half a step."""
+    _require_cuda(bits)
+    if bits.dtype != torch.uint32 or bits.dim() != 2:
+        raise ValueError("bits must be a 2-D uint32 tensor")
+    n = bits.shape[0]
+    tr = trellis(L, seq_len)
+    words = int(lib().tcq_stream_words(ctypes.byref(tr), int(layout)))
+    if words == 0:
+        raise TcqError(_abi.TCQ_ERR_UNSUPPORTED, "tcq_stream_words")
+    if bits.shape[1] != words:
+        raise ValueError(f"bits must have {words} words per sequence for this trellis and layout")
+    shape = (rows, cols) if out_layout == OUT_TILE16 else (n, seq_len)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int8, device=bits.device)
+    else:
+        _out(out, shape, torch.int8, bits)
+    check(lib().tcq_decode_int8(ctypes.byref(tr), _ptr(bits), n, int(layout), int(out_layout),
+                                int(rows), int(cols), _ptr(out), _stream()), "tcq_decode_int8")
+    return out
+
+
+def _int8_operands(a, a_scale, weights, bias=None):
+    """Shapes and types of an int8 product's operands; returns (n_tok, n_out, n_in)."""
+    _require_cuda(a, a_scale, *(t for pair in weights for t in pair), bias)
+    if a.dim() != 2 or a.dtype != torch.int8:
+        raise ValueError("a must be a 2-D int8 tensor [n_tok, n_in]")
+    n_tok, n_in = a.shape
+    n_out = weights[0][0].shape[0]
+    for w, ws in weights:
+        if w.dtype != torch.int8 or w.shape != (n_out, n_in):
+            raise ValueError(f"weights must be int8 tensors of one shape [n_out, {n_in}]")
+        if ws.dtype != torch.float32 or ws.shape != (n_out,):
+            raise ValueError(f"a weight's scale must be a float32 tensor [{n_out}]")
+    if a_scale.dtype != torch.float32 or a_scale.shape != (n_tok,):
+        raise ValueError(f"a_scale must be a float32 tensor [{n_tok}]")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (n_out,)):
+        raise ValueError(f"bias must be a float32 tensor [{n_out}]")
+    return n_tok, n_out, n_in
+
+
+def _result(out, shape, dtype, like):
+    if dtype not in _DTYPE:
+        raise ValueError("the output type must be float16, bfloat16 or float32")
+    return (torch.empty(shape, dtype=dtype, device=like.device) if out is None
+            else _out(out, shape, dtype, like))
+
+
+def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float16,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """out[m, n] = a_scale[m] w_scale[n] (a w^T)[m, n] + bias[n] for int8
+    tokens ``a`` [n_tok, n_in] and weights ``w`` [n_out, n_in] with fp32
+    scales; the product is exact in 32-bit integers."""
+    n_tok, n_out, n_in = _int8_operands(a, a_scale, ((w, w_scale),), bias)
+    out = _result(out, (n_tok, n_out), out_dtype, a)
+    need = int(lib().tcq_int8_matmul_workspace_size(n_tok, n_out, n_in))
+    ws = _use_workspace(workspace, need, a) if need else None
+    check(lib().tcq_int8_matmul(_ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(bias), n_tok,
+                                n_out, n_in, _ptr(out), _DTYPE[out_dtype], _ptr(ws),
+                                _nbytes(ws) if need else 0, _stream()), "tcq_int8_matmul")
+    return out
+
+
+def int8_gated_ffn(a: torch.Tensor, a_scale: torch.Tensor, w_gate: torch.Tensor,
+                   w_gate_scale: torch.Tensor, w_up: torch.Tensor, w_up_scale: torch.Tensor,
+                   act: int = ACT_SILU, out_dtype: torch.dtype = torch.float16,
+                   out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated feed-forward block on int8 operands: act(g) * u with g and u
+    the scaled int8 products of ``a`` with ``w_gate`` and ``w_up``."""
+    n_tok, n_out, n_in = _int8_operands(a, a_scale, ((w_gate, w_gate_scale), (w_up, w_up_scale)))
+    out = _result(out, (n_tok, n_out), out_dtype, a)
+    need = int(lib().tcq_int8_gated_ffn_workspace_size(n_tok, n_out, n_in))
+    ws = _use_workspace(workspace, need, a) if need else None
+    check(lib().tcq_int8_gated_ffn(_ptr(a), _ptr(a_scale), _ptr(w_gate), _ptr(w_gate_scale),
+                                   _ptr(w_up), _ptr(w_up_scale), n_tok, n_out, n_in, int(act),
+                                   _ptr(out), _DTYPE[out_dtype], _ptr(ws),
+                                   _nbytes(ws) if need else 0, _stream()), "tcq_int8_gated_ffn")
+    return out
+
+
+def _ffn_operands(x, w_gate, w_up):
+    _require_cuda(x, w_gate, w_up)
+    if x.dim() != 2 or x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("x must be a 2-D float16 or bfloat16 tensor [n_tok, n_in]")
+    n_tok, n_in = x.shape
+    if w_gate.dim() != 2 or w_gate.shape[1] != n_in or w_up.shape != w_gate.shape:
+        raise ValueError(f"w_gate and w_up must be tensors of one shape [n_out, {n_in}]")
+    if w_gate.dtype != x.dtype or w_up.dtype != x.dtype:
+        raise ValueError(f"w_gate and w_up must be {x.dtype} like x")
+    return n_tok, w_gate.shape[0], n_in
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: int = ACT_SILU,
+              out: torch.Tensor | None = None, save: bool = False,
+              workspace: torch.Tensor | None = None):
+    """h = act(x w_gate^T) * (x w_up^T) for fp16 or bf16 tokens ``x`` [n_tok,
+    n_in] and weights [n_out, n_in], sums and activation in fp32.  With
+    ``save=True`` returns (h, gate, up), the fp32 projections that
+    ``gated_ffn_backward`` takes."""
+    n_tok, n_out, n_in = _ffn_operands(x, w_gate, w_up)
+    out = _result(out, (n_tok, n_out), x.dtype, x)
+    gate = up = None
+    if save:
+        gate, up = (torch.empty((n_tok, n_out), dtype=torch.float32, device=x.device) for _ in range(2))
+    need = int(lib().tcq_gated_ffn_workspace_size(n_tok, n_out, n_in))
+    ws = _use_workspace(workspace, need, x) if need else None
+    check(lib().tcq_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _DTYPE[x.dtype], n_tok, n_out, n_in,
+                              int(act), _ptr(out), _ptr(gate), _ptr(up), _ptr(ws),
+                              _nbytes(ws) if need else 0, _stream()), "tcq_gated_ffn")
+    return (out, gate, up) if save else out
+
+
+def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                       gate: torch.Tensor, up: torch.Tensor, grad_out: torch.Tensor,
+                       act: int = ACT_SILU, need: "tuple[bool, bool, bool]" = (True, True, True),
+                       workspace: torch.Tensor | None = None):
+    """Gradients of ``gated_ffn`` for the output gradient ``grad_out`` and the
+    saved ``gate`` and ``up``; returns (grad_x, grad_w_gate, grad_w_up), None
+    where ``need`` is false."""
+    n_tok, n_out, n_in = _ffn_operands(x, w_gate, w_up)
+    _require_cuda(x, gate, up, grad_out)
+    if any(t.shape != (n_tok, n_out) or t.dtype != torch.float32 for t in (gate, up)):
+        raise ValueError(f"gate and up must be float32 tensors [{n_tok}, {n_out}]")
+    if grad_out.shape != (n_tok, n_out) or grad_out.dtype != x.dtype:
+        raise ValueError(f"grad_out must be a {x.dtype} tensor [{n_tok}, {n_out}]")
+    grads = [torch.empty_like(t) if n else None for t, n in zip((x, w_gate, w_up), need)]
+    size = int(lib().tcq_gated_ffn_backward_workspace_size(n_tok, n_out, n_in))
+    ws = _use_workspace(workspace, size, x)
+    check(lib().tcq_gated_ffn_backward(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up),
+                                       _ptr(grad_out), _DTYPE[x.dtype], n_tok, n_out, n_in, int(act),
+                                       _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]), _ptr(ws),
+                                       _nbytes(ws), _stream()), "tcq_gated_ffn_backward")
+    return tuple(grads)
+
+
+class GatedFfn(torch.autograd.Function):
+    """h = GatedFfn.apply(x, w_gate, w_up, act): ``gated_ffn`` with its
+    gradients.  It keeps the two projections in fp32 for the backward pass (8
+    bytes a hidden value; rounded to 16 bits they would cost the gradients
+    more than the rounding of their own operands).  Twice differentiable it is
+    not: a second derivative raises."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, act=ACT_SILU):
+        if not any(ctx.needs_input_grad[:3]):
+            return gated_ffn(x, w_gate, w_up, act)
+        h, gate, up = gated_ffn(x, w_gate, w_up, act, save=True)
+        ctx.save_for_backward(x, w_gate, w_up, gate, up)
+        ctx.act = act
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        grad_out = grad_out.contiguous()
+        if grad_out.data_ptr() % 16:                 # a slice of a larger gradient may start anywhere
+            grad_out = grad_out.clone()
+        grads = gated_ffn_backward(*ctx.saved_tensors, grad_out, ctx.act,
+                                   need=ctx.needs_input_grad[:3])
+        return (*grads, None)

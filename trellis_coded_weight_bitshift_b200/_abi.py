@@ -17,6 +17,13 @@ TAILBITING = 0
 FREE_START = 1
 OUT_SEQ = 0
 OUT_TILE16 = 1
+F16 = 0
+BF16 = 1
+F32 = 2
+ACT_SILU = 0
+ACT_GELU = 1
+ACT_GELU_TANH = 2
+ACT_RELU = 3
 
 EXPORTS = (
     "tcq_version", "tcq_status_string", "tcq_stream_words",
@@ -24,6 +31,9 @@ EXPORTS = (
     "tcq_viterbi_encode_tailbiting",
     "tcq_bcjr_workspace_size", "tcq_bcjr_soft", "tcq_bcjr_soft_backward", "tcq_bcjr_soft_and_grad",
     "tcq_pack_states", "tcq_decode", "tcq_decode_gemv", "tcq_rht",
+    "tcq_quantize_int8", "tcq_decode_int8", "tcq_int8_matmul_workspace_size", "tcq_int8_matmul",
+    "tcq_gated_ffn_workspace_size", "tcq_gated_ffn", "tcq_gated_ffn_backward_workspace_size",
+    "tcq_gated_ffn_backward", "tcq_int8_gated_ffn_workspace_size", "tcq_int8_gated_ffn",
 )
 
 
@@ -78,6 +88,22 @@ def lib() -> ctypes.CDLL:
     L.tcq_rht.argtypes = [P, I64, I64, P, P, P, P]
     L.tcq_decode.restype = I
     L.tcq_decode.argtypes = [TP, P, I64, I, I, I64, I64, P, P]
+    L.tcq_quantize_int8.restype = I
+    L.tcq_quantize_int8.argtypes = [P, I, I64, I64, P, P, P]
+    L.tcq_decode_int8.restype = I
+    L.tcq_decode_int8.argtypes = [TP, P, I64, I, I, I64, I64, P, P]
+    for name in ("int8_matmul", "gated_ffn", "gated_ffn_backward", "int8_gated_ffn"):
+        size = getattr(L, f"tcq_{name}_workspace_size")
+        size.restype = SZ
+        size.argtypes = [I64, I64, I64]
+    L.tcq_int8_matmul.restype = I
+    L.tcq_int8_matmul.argtypes = [P, P, P, P, P, I64, I64, I64, P, I, P, SZ, P]
+    L.tcq_gated_ffn.restype = I
+    L.tcq_gated_ffn.argtypes = [P, P, P, I, I64, I64, I64, I, P, P, P, P, SZ, P]
+    L.tcq_gated_ffn_backward.restype = I
+    L.tcq_gated_ffn_backward.argtypes = [P, P, P, P, P, P, I, I64, I64, I64, I, P, P, P, P, SZ, P]
+    L.tcq_int8_gated_ffn.restype = I
+    L.tcq_int8_gated_ffn.argtypes = [P, P, P, P, P, P, I64, I64, I64, I, P, I, P, SZ, P]
     return L
 
 
