@@ -327,6 +327,13 @@ TCQ_API tcq_status_t tcq_rht(const float *W, int64_t rows, int64_t cols, const f
  * one of a weight row the outputs of its channel (and grad_x).
  * Results do not depend on what else runs and repeat bit for bit.
  * ------------------------------------------------------------------------ */
+
+/* How often a product's kernel gave up waiting for its own loads or products
+ * (two seconds each) on the current device since the library was loaded: 0
+ * unless something is wrong; the outputs of such a call are unspecified.
+ * Waits for the device. */
+TCQ_API tcq_status_t tcq_products_gave_up(unsigned int *count);
+
 enum { TCQ_F16 = 0, TCQ_BF16 = 1, TCQ_F32 = 2 };
 
 /* Activations: v / (1 + e^-v); v Phi(v) (normal distribution function); its

@@ -44,7 +44,7 @@ __all__ = [
     "quantize_int8", "decode_int8", "int8_matmul", "gated_ffn", "gated_ffn_backward", "GatedFfn",
     "int8_gated_ffn", "DECODE_INT8_SCALE", "int8_matmul_workspace_size", "gated_ffn_workspace_size",
     "gated_ffn_backward_workspace_size", "int8_gated_ffn_workspace_size",
-    "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "ACT_RELU",
+    "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "ACT_RELU", "products_gave_up",
 ]
 
 # one step of decode_int8 in units of the 1MAD code: (bytesum - 510) / 147.8 = 4 q / 147.8
@@ -328,6 +328,14 @@ def decode_gemv(bits: torch.Tensor, x: torch.Tensor, rows: int, cols: int, L: in
     check(lib().tcq_decode_gemv(ctypes.byref(tr), _ptr(bits), int(layout), int(rows), int(cols),
                                 _ptr(x), _ptr(y), _stream()), "tcq_decode_gemv")
     return y
+
+
+def products_gave_up() -> int:
+    """How often a product's kernel on the current device gave up a wait of
+    its own (0 unless something is wrong); waits for the device."""
+    count = ctypes.c_uint()
+    check(lib().tcq_products_gave_up(ctypes.byref(count)), "tcq_products_gave_up")
+    return count.value
 
 
 def int8_matmul_workspace_size(n_tok: int, n_out: int, n_in: int) -> int:

@@ -34,6 +34,7 @@ EXPORTS = (
     "tcq_quantize_int8", "tcq_decode_int8", "tcq_int8_matmul_workspace_size", "tcq_int8_matmul",
     "tcq_gated_ffn_workspace_size", "tcq_gated_ffn", "tcq_gated_ffn_backward_workspace_size",
     "tcq_gated_ffn_backward", "tcq_int8_gated_ffn_workspace_size", "tcq_int8_gated_ffn",
+    "tcq_products_gave_up",
 )
 
 
@@ -88,6 +89,8 @@ def lib() -> ctypes.CDLL:
     L.tcq_rht.argtypes = [P, I64, I64, P, P, P, P]
     L.tcq_decode.restype = I
     L.tcq_decode.argtypes = [TP, P, I64, I, I, I64, I64, P, P]
+    L.tcq_products_gave_up.restype = I
+    L.tcq_products_gave_up.argtypes = [ctypes.POINTER(ctypes.c_uint)]
     L.tcq_quantize_int8.restype = I
     L.tcq_quantize_int8.argtypes = [P, I, I64, I64, P, P, P]
     L.tcq_decode_int8.restype = I

@@ -1,100 +1,401 @@
 // Matrix products on decoded weights: int8 with token and channel scales, and
 // the gated feed-forward block with its gradients.
 //
-// Plain tiles: a 256-thread block computes 32 x 32 results, four a thread,
-// with 32-deep slices of both operands in shared memory.
+// pair_kernel: persistent, two blocks of a cluster (two SMs) work on one tile
+// of 256 x 256 results.  Each block loads its 128 rows of A and its half of B
+// (128 rows) by tensor-map loads into a ring of 32 KB stages; one thread of the
+// first block issues tcgen05.mma for the pair (M = 256, N = 256, 32 bytes of the
+// contraction each); the sums stay in tensor memory, two tiles of them (2 x 256
+// columns), so that eight warps a block write one tile out while the next is
+// computed.  In the gated block the halves of B are 128 channels of Wg and the
+// same 128 of Wu: both projections of a result lie in one thread's tensor-memory
+// lane, and act(g) * u needs no exchange.
+//
+// Why this split: a 256 x 256 tile reads 64 KB of operands for each 64-deep
+// 16-bit step (8 MFLOP), which neither the shared-memory port (64 of 128 bytes a
+// clock) nor L2 limits; a 128 x 128 tile of one block would need all of the port.
 #include <algorithm>
 #include <cuda_bf16.h>
 
 #include "tcq_activation.cuh"
-#include "tcq_device.cuh"
+#include "tcq_tensor.cuh"
 
 namespace tcq {
 
-template <typename T> struct Sum { typedef float type; };
-template <> struct Sum<int8_t> { typedef int type; };
-template <typename T> __device__ __forceinline__ typename Sum<T>::type widen(T v);
-template <> __device__ __forceinline__ int widen<int8_t>(int8_t v) { return v; }
-template <> __device__ __forceinline__ float widen<__half>(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+constexpr int kStages = 6, kStageBytes = 32768, kPairThreads = 320;
+constexpr int kPairSmem = kStages * kStageBytes + 1024;
 
-// An operand's element (i, k) at p[i * si + k * sk].
-template <typename T> struct Operand {
-  const T *p;
-  int64_t si, sk;
+// One product: sums over `segs` pairs of operands a[s], b[s] in turn, or (z > 1)
+// z products with operands a[z] and the same b[0].
+struct Job {
+  CUtensorMap a[2], b[2];
+  void *out[2];
+  int64_t M, N;        // results of one product
+  int mt, nt;          // tiles of it
+  int kb, segs;        // steps of one segment
+  int z;
+  int a_mn, b_mn;      // operand stored with its rows along the contraction
+  int wide;            // bytes of a store: 32, 16 or one element
 };
 
-__device__ __forceinline__ void store(void *out, int64_t i, int dtype, float v) {
-  if (dtype == TCQ_F16) ((__half *)out)[i] = __float2half_rn(v);
-  else if (dtype == TCQ_BF16) ((__nv_bfloat16 *)out)[i] = __float2bfloat16_rn(v);
-  else ((float *)out)[i] = v;
-}
+// Tiles [lo, hi) of a job, dealt in turn to clusters first .. first + n - 1.
+struct Share {
+  int job, first, n;
+  int64_t lo, hi;
+};
 
-struct Out {
-  void *out;
+struct Epilogue {
   int dtype, act;
   const float *a_scale, *s0, *s1, *bias;
   float *gate, *up;
+  int wide_save;
 };
 
-// DUAL: both products share a0 and end in act(g) * u; else a1, b1 (if any) add
-// to the same sums.
-template <typename T, bool DUAL>
-__global__ void __launch_bounds__(256) product_kernel(Operand<T> a0, Operand<T> b0, Operand<T> a1, Operand<T> b1,
-                                                      int64_t M, int64_t N, int64_t K, Out o) {
-  typedef typename Sum<T>::type S;
-  __shared__ S as[32][33], bs[32][33], cs[32][33];
-  const int64_t n0 = (int64_t)blockIdx.x * 32;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  for (int64_t m0 = (int64_t)blockIdx.y * 32; m0 < M; m0 += (int64_t)gridDim.y * 32) {
-    S acc[4] = {}, acc2[4] = {};
-    for (int seg = 0; seg < (!DUAL && b1.p ? 2 : 1); ++seg) {
-      const Operand<T> a = seg ? a1 : a0, b = seg ? b1 : b0;
-      for (int64_t k0 = 0; k0 < K; k0 += 32) {
-        for (int r = ty; r < 32; r += 8) {
-          const int64_t k = k0 + tx;
-          as[r][tx] = m0 + r < M && k < K ? widen<T>(a.p[(m0 + r) * a.si + k * a.sk]) : S(0);
-          bs[r][tx] = n0 + r < N && k < K ? widen<T>(b.p[(n0 + r) * b.si + k * b.sk]) : S(0);
-          if (DUAL) cs[r][tx] = n0 + r < N && k < K ? widen<T>(b1.p[(n0 + r) * b1.si + k * b1.sk]) : S(0);
-        }
-        __syncthreads();
-        for (int k = 0; k < 32; ++k)
-          for (int j = 0; j < 4; ++j) {
-            acc[j] += as[ty + 8 * j][k] * bs[tx][k];
-            if (DUAL) acc2[j] += as[ty + 8 * j][k] * cs[tx][k];
-          }
-        __syncthreads();
-      }
+struct PairParams {
+  Job job[2];
+  Share share[3];
+  int shares;
+  int bf16;
+  Epilogue e;
+};
+
+// The tiles of one cluster, in order.
+struct Tiles {
+  int s;
+  int64_t t;
+  __device__ __forceinline__ Tiles() : s(-1), t(0) {}
+  __device__ __forceinline__ bool next(const PairParams &p, int cluster) {
+    if (s >= 0) {
+      t += p.share[s].n;
+      if (t < p.share[s].hi) return true;
     }
-    const int64_t n = n0 + tx;
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 8 * j;
-      if (m >= M || n >= N) continue;
-      float g = (float)acc[j], u = (float)acc2[j];
-      if (o.a_scale) {
-        g = g * o.a_scale[m] * o.s0[n];
-        if (DUAL) u = u * o.a_scale[m] * o.s1[n];
-      }
-      if (o.bias) g = __fadd_rn(g, o.bias[n]);
-      if (DUAL && o.gate) {
-        o.gate[m * N + n] = g;
-        o.up[m * N + n] = u;
-      }
-      store(o.out, m * N + n, o.dtype, DUAL ? activation(g, o.act) * u : g);
+    while (++s < p.shares) {
+      const int c = cluster - p.share[s].first;
+      t = p.share[s].lo + c;
+      if (c >= 0 && c < p.share[s].n && t < p.share[s].hi) return true;
     }
+    return false;
+  }
+  // Bands of eight row tiles, rows first, so that clusters at work share operands in L2.
+  __device__ __forceinline__ void place(const Job &j, int &z, int &m, int &n) const {
+    const int64_t per = (int64_t)j.mt * j.nt;
+    z = j.z > 1 ? (int)(t / per) : 0;
+    const int64_t r = t - z * per, band = r / (8 * (int64_t)j.nt), in = r - band * 8 * j.nt;
+    const int rows = min(8, j.mt - (int)band * 8);
+    m = (int)band * 8 + (int)(in % rows);
+    n = (int)(in / rows);
+  }
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
+  if (dtype == TCQ_F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void store_words(char *p, const uint32_t (&v)[8], int wide) {
+  if (wide == 32) {
+    store32(p, v);
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
 }
 
+// Sixteen neighbouring results of one row, the first `n` of them inside the matrix.
+__device__ __forceinline__ void store16(void *out, int64_t at, int dtype, const float (&v)[16], int n, int wide) {
+  if (n >= 16 && wide >= 16) {
+    uint32_t w[8];
+    if (dtype == TCQ_F32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+        store_words((char *)out + 4 * at + 32 * h, w, wide);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], dtype);
+      store_words((char *)out + 2 * at, w, wide);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (i >= n) continue;
+    if (dtype == TCQ_F32) ((float *)out)[at + i] = v[i];
+    else ((uint16_t *)out)[at + i] = (uint16_t)pack2(v[i], 0.0f, dtype);
+  }
+}
+
+// Sixteen channels' scales (or biases) from channel n on, `valid` of them there.
+__device__ __forceinline__ void channel16(const float *s, int64_t n, int valid, float (&v)[16]) {
+  if (valid >= 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 q = __ldg(reinterpret_cast<const float4 *>(s + n) + i);
+      v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < valid ? __ldg(s + n + i) : 0.0f;
+  }
+}
+
+// Sums as fp32 (an int32 sum is rounded to fp32 here), scaled.
+template <bool I8>
+__device__ __forceinline__ void finish16(float (&v)[16], const float *s, int64_t n, int valid, float sa) {
+  if (!I8) return;
+  float c[16];
+  channel16(s, n, valid, c);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = (float)__float_as_int(v[i]) * sa * c[i];
+}
+
+template <bool I8, bool DUAL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_kernel(const __grid_constant__ PairParams p) {
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t stop;
+  const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
+                 acc_empty = acc_full + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1;
+
+  if (threadIdx.x == 0) {
+    stop = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, 16);                  // eight warps in each block
+    }
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), 512);
+  tmem_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tmem_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    // ---- loads: this block's rows of A and half of B, counted by the first block's barrier
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    Tiles it;
+    while (ok && it.next(p, cluster)) {
+      const Job &j = p.job[p.share[it.s].job];
+      int z, m, n;
+      it.place(j, z, m, n);
+      const int row = m * 256 + (int)rank * 128;
+      const int col = DUAL ? n * 128 : n * 256 + (int)rank * 128;
+      const CUtensorMap *bd = DUAL ? &j.b[rank] : nullptr;
+      for (int kb = 0; kb < j.kb * j.segs; ++kb) {
+        if (!mbar_wait(empty + 8 * s, ph ^ 1, &stop)) { ok = false; break; }
+        const int seg = kb >= j.kb ? 1 : 0;
+        const int k = (kb - seg * j.kb) * (I8 ? 128 : 64);
+        const uint32_t bar = map_to_rank(full + 8 * s, 0);
+        const uint32_t a = ring + s * kStageBytes, b = a + 16384;
+        if (rank == 0) mbar_expect(full + 8 * s, 2 * kStageBytes);
+        const CUtensorMap *am = &j.a[seg + z], *bm = DUAL ? bd : &j.b[seg];
+        if (!j.a_mn) {
+          tma_load_pair(a, am, k, row, bar);
+        } else {
+          tma_load_pair(a, am, row, k, bar);
+          tma_load_pair(a + 8192, am, row + 64, k, bar);
+        }
+        if (!j.b_mn) {
+          tma_load_pair(b, bm, k, col, bar);
+        } else {
+          tma_load_pair(b, bm, col, k, bar);
+          tma_load_pair(b + 8192, bm, col + 64, k, bar);
+        }
+        if (++s == kStages) { s = 0; ph ^= 1; }
+      }
+    }
+    if (ok) {
+      // the last products' releases arrive while this block is still there
+      for (int i = 0; i < kStages && ok; ++i) {
+        ok = mbar_wait(empty + 8 * s, ph ^ 1, &stop);
+        if (++s == kStages) { s = 0; ph ^= 1; }
+      }
+    } else if (rank == 0) {
+      // gave up: the copies in flight land first (each wait limited)
+      for (int i = 0; i < kStages; ++i) {
+        s = s ? s - 1 : kStages - 1;
+        if (s == kStages - 1) ph ^= 1;
+        const unsigned long long t0 = now_ns();
+        while (!mbar_try(full + 8 * s, ph) && now_ns() - t0 < kWaitNs / 16) {}
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---- products
+    int s = 0, n_acc = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    Tiles it;
+    while (ok && it.next(p, cluster)) {
+      const Job &j = p.job[p.share[it.s].job];
+      const int buf = n_acc & 1;
+      if (!mbar_wait(acc_empty + 8 * buf, ((n_acc >> 1) & 1) ^ 1, &stop)) break;
+      tmem_fence_after_sync();
+      const uint32_t d = tmem + buf * 256;
+      const uint32_t instr = I8 ? instr_i8(256, 256) : instr_f16(256, 256, p.bf16, j.a_mn, j.b_mn);
+      const uint32_t a_step = j.a_mn ? 2048 >> 4 : 32 >> 4, b_step = j.b_mn ? 2048 >> 4 : 32 >> 4;
+      for (int kb = 0; kb < j.kb * j.segs; ++kb) {
+        if (!mbar_wait(full + 8 * s, ph, &stop)) { ok = false; break; }
+        tmem_fence_after_sync();
+        const uint32_t at = ring + s * kStageBytes;
+        uint64_t a = operand_desc(at, j.a_mn), b = operand_desc(at + 16384, j.b_mn);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mma<I8, true>(d, a, b, instr, kb > 0 || i > 0);
+          a += a_step;
+          b += b_step;
+        }
+        mma_commit_pair(empty + 8 * s);
+        if (++s == kStages) { s = 0; ph ^= 1; }
+      }
+      mma_commit_pair(acc_full + 8 * buf);
+      ++n_acc;
+    }
+  } else if (warp >= 2) {
+    // ---- results: warp w reads the lanes of quarter w % 4, one half of the columns
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    int n_acc = 0;
+    Tiles it;
+    while (it.next(p, cluster)) {
+      const Job &j = p.job[p.share[it.s].job];
+      int z, m, n;
+      it.place(j, z, m, n);
+      const int buf = n_acc & 1;
+      const bool got = mbar_wait(acc_full + 8 * buf, (n_acc >> 1) & 1, &stop);
+      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      tmem_fence_after_sync();
+      const int64_t row = (int64_t)m * 256 + rank * 128 + quarter * 32 + lane;
+      const bool in = row < j.M;
+      const float sa = I8 && in ? __ldg(p.e.a_scale + row) : 1.0f;
+      const uint32_t t0 = tmem + buf * 256 + ((uint32_t)quarter << 21);
+      constexpr int kChunks = DUAL ? 4 : 8;
+      const int col0 = half * (DUAL ? 64 : 128);
+      const int64_t n0 = (int64_t)n * (DUAL ? 128 : 256) + col0;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c) {
+        const int64_t ch = n0 + 16 * c;
+        const int valid = (int)min((int64_t)16, j.N - ch);
+        float g[16], u[16];
+        __syncwarp();                                    // rows past the end skipped the last stores
+        tmem_ld16(t0 + col0 + 16 * c, g);
+        if (DUAL) tmem_ld16(t0 + 128 + col0 + 16 * c, u);
+        tmem_wait_ld();
+        if (c == kChunks - 1) {                          // the tile's sums are in registers: the buffer is free
+          tmem_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(acc_empty + 8 * buf, 0);
+        }
+        if (!in || valid <= 0) continue;
+        const int64_t at = row * j.N + ch;
+        finish16<I8>(g, p.e.s0, ch, valid, sa);
+        if (DUAL) {
+          finish16<I8>(u, p.e.s1, ch, valid, sa);
+          if (!I8 && p.e.gate) {
+            store16(p.e.gate, at, TCQ_F32, g, valid, p.e.wide_save);
+            store16(p.e.up, at, TCQ_F32, u, valid, p.e.wide_save);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) g[i] = activation(g[i], p.e.act) * u[i];
+        } else if (I8 && p.e.bias) {
+          float b[16];
+          channel16(p.e.bias, ch, valid, b);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) g[i] = __fadd_rn(g[i], b[i]);
+        }
+        store16(j.out[z], at, p.e.dtype, g, valid, j.wide);
+      }
+      ++n_acc;
+    }
+  }
+  __syncwarp();
+  tmem_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (threadIdx.x == 0 && stop) atomicAdd(&g_gave_up, 1u);
+}
+
+// Rows of `bytes` bytes, packed, to rows `pitch` bytes apart (a multiple of 16),
+// 16 bytes a thread.  The source is read in whole aligned words; the last row's
+// end is read by bytes, so nothing past it is touched.
+__global__ void __launch_bounds__(256) pitch_rows_kernel(const uint8_t *__restrict__ src, int64_t rows, int64_t bytes,
+                                                         int64_t pitch, uint4 *__restrict__ dst) {
+  const int64_t per = pitch >> 4, n = rows * per, total = rows * bytes;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per, c = (i - r * per) << 4;
+    const int64_t at = r * bytes + c, last = min(at + 16, r * bytes + bytes);   // [at, last) is wanted
+    const int64_t w0 = at & ~(int64_t)3;
+    uint32_t w[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      const int64_t b = w0 + 4 * k;
+      w[k] = 0;
+      if (b + 4 <= total) {
+        if (b < last) w[k] = __ldg(reinterpret_cast<const uint32_t *>(src + b));
+      } else {
+        for (int q = 0; q < 4; ++q)
+          if (b + q < total) w[k] |= (uint32_t)src[b + q] << (8 * q);
+      }
+    }
+    const uint32_t sh = 8 * (uint32_t)(at & 3);
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      o[k] = __funnelshift_r(w[k], w[k + 1], sh);
+      const int64_t left = last - (at + 4 * k);                                  // bytes of this word inside the row
+      if (left <= 0) o[k] = 0;
+      else if (left < 4) o[k] &= (1u << (8 * (int)left)) - 1u;
+    }
+    dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+template <typename T> __device__ __forceinline__ float widen(T v);
+template <> __device__ __forceinline__ float widen<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T narrow(float v);
+template <> __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// dg = grad u act'(g), du = grad act(g), in rows `pitch` elements apart.
 template <typename T>
 __global__ void __launch_bounds__(256) gate_grad_kernel(const T *__restrict__ grad, const float *__restrict__ gate,
-                                                        const float *__restrict__ up, int64_t n, int act,
-                                                        T *__restrict__ dg, T *__restrict__ du) {
+                                                        const float *__restrict__ up, int64_t rows, int64_t cols,
+                                                        int64_t pitch, int act, T *__restrict__ dg,
+                                                        T *__restrict__ du) {
+  const int64_t n = rows * cols;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cols, c = i - r * cols;
     float a, d;
     activation_slope(gate[i], act, a, d);
     const float h = widen<T>(grad[i]);
-    store(dg, i, sizeof(T) == 2 && std::is_same<T, __half>::value ? TCQ_F16 : TCQ_BF16, h * up[i] * d);
-    store(du, i, sizeof(T) == 2 && std::is_same<T, __half>::value ? TCQ_F16 : TCQ_BF16, h * a);
+    dg[r * pitch + c] = narrow<T>(h * up[i] * d);
+    du[r * pitch + c] = narrow<T>(h * a);
   }
 }
 
@@ -103,127 +404,211 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const T *__restrict__ gr
 using namespace tcq;
 using namespace tcq_host;
 
-static bool size_ok(int64_t n) { return n < (1ll << 30); }
+namespace {
 
-static bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+constexpr int64_t kMostIn8 = 131071, kMost = (1ll << 30) - 1;
 
-static tcq_status_t check_sizes(int64_t n_tok, int64_t n_out, int64_t n_in, int64_t most_in) {
+tcq_status_t check_sizes(int64_t n_tok, int64_t n_out, int64_t n_in, int64_t most_in) {
   if (n_tok < 0 || n_out <= 0 || n_in <= 0) return TCQ_ERR_INVALID_ARG;
-  if (!size_ok(n_tok) || !size_ok(n_out) || n_in > most_in) return TCQ_ERR_UNSUPPORTED;
+  if (n_tok > kMost || n_out > kMost || n_in > most_in) return TCQ_ERR_UNSUPPORTED;
   return TCQ_OK;
 }
 
-static bool bad_ptr(const void *p) { return !p || !aligned16(p); }
+bool bad_ptr(const void *p) { return !p || !aligned16(p); }
+bool bad_type(int t) { return t != TCQ_F16 && t != TCQ_BF16 && t != TCQ_F32; }
+bool bad_act(int a) { return a < TCQ_ACT_SILU || a > TCQ_ACT_RELU; }
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t tiles(int64_t n, int64_t by) { return (n + by - 1) / by; }
+unsigned blocks_for(int64_t threads) {
+  return (unsigned)std::min<int64_t>((threads + 255) / 256, (int64_t)sm_count() * 16);
+}
+int width(const void *p, int64_t cols, int size) {
+  const uint64_t v = (uint64_t)reinterpret_cast<uintptr_t>(p) | (uint64_t)(cols * size);
+  return v % 32 == 0 ? 32 : v % 16 == 0 ? 16 : size;
+}
+int type_size(int t) { return t == TCQ_F32 ? 4 : 2; }
 
-template <typename T, bool DUAL>
-static tcq_status_t run_product(Operand<T> a0, Operand<T> b0, Operand<T> a1, Operand<T> b1, int64_t M, int64_t N,
-                                int64_t K, const Out &o, cudaStream_t s) {
-  const dim3 grid((unsigned)((N + 31) / 32), (unsigned)std::min<int64_t>((M + 31) / 32, 65535));
-  product_kernel<T, DUAL><<<grid, 256, 0, s>>>(a0, b0, a1, b1, M, N, K, o);
+// Whether a packed matrix of rows of `bytes` bytes has to be copied to an
+// aligned pitch for tensor-map loads, and what the copy takes.
+bool needs_pitch(int64_t rows, int64_t bytes) { return rows > 1 && bytes % 16 != 0; }
+size_t pitch_bytes(int64_t rows, int64_t bytes) {
+  return needs_pitch(rows, bytes) ? round256((size_t)rows * round_up(bytes, 16)) : 0;
+}
+
+// An operand ready for tensor-map loads: where it is and its pitch.
+struct Operand {
+  const void *p;
+  int64_t rows, cols, pitch;
+  int es;
+};
+
+struct Workspace {
+  char *at;
+  void *take(size_t n) {
+    void *p = at;
+    at += round256(n);
+    return p;
+  }
+};
+
+tcq_status_t ready(Operand &o, const void *p, int64_t rows, int64_t cols, int es, Workspace &ws, cudaStream_t s) {
+  o = {p, rows, cols, round_up(cols * es, 16), es};
+  if (!needs_pitch(rows, cols * es)) return TCQ_OK;
+  uint4 *copy = (uint4 *)ws.take(pitch_bytes(rows, cols * es));
+  pitch_rows_kernel<<<blocks_for(rows * (o.pitch / 16)), 256, 0, s>>>((const uint8_t *)p, rows, cols * es, o.pitch,
+                                                                      copy);
+  o.p = copy;
   return launch_status();
 }
 
-extern "C" size_t tcq_int8_matmul_workspace_size(int64_t, int64_t, int64_t) { return 0; }
-extern "C" size_t tcq_gated_ffn_workspace_size(int64_t, int64_t, int64_t) { return 0; }
-extern "C" size_t tcq_int8_gated_ffn_workspace_size(int64_t, int64_t, int64_t) { return 0; }
+bool map_of(CUtensorMap *m, const Operand &o, int box_rows) {
+  return make_map(m, o.p, o.es, o.rows, o.cols, o.pitch, box_rows);
+}
+
+template <bool I8, bool DUAL>
+tcq_status_t launch_pair(PairParams &p, cudaStream_t s) {
+  if (cudaFuncSetAttribute(pair_kernel<I8, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) !=
+      cudaSuccess)
+    return TCQ_ERR_CUDA;
+  const int clusters = std::max(1, sm_count() / 2);
+  int64_t most = 0;
+  if (p.shares == 0) {                                   // one job, dealt over all clusters
+    const int64_t n = (int64_t)p.job[0].mt * p.job[0].nt * p.job[0].z;
+    p.share[0] = {0, 0, clusters, 0, n};
+    p.shares = 1;
+    most = n;
+  } else {
+    most = clusters;
+  }
+  const unsigned grid = 2 * (unsigned)std::min<int64_t>(clusters, most);
+  if (p.shares == 1) p.share[0].n = (int)(grid / 2);
+  pair_kernel<I8, DUAL><<<grid, kPairThreads, kPairSmem, s>>>(p);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" tcq_status_t tcq_products_gave_up(unsigned int *count) {
+  if (!count) return TCQ_ERR_INVALID_ARG;
+  return cudaMemcpyFromSymbol(count, g_gave_up, sizeof(unsigned)) == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA;
+}
+
+extern "C" size_t tcq_int8_matmul_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
+  if (check_sizes(n_tok, n_out, n_in, kMostIn8) != TCQ_OK) return 0;
+  return pitch_bytes(n_tok, n_in) + pitch_bytes(n_out, n_in);
+}
+
+extern "C" size_t tcq_int8_gated_ffn_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
+  if (check_sizes(n_tok, n_out, n_in, kMostIn8) != TCQ_OK) return 0;
+  return pitch_bytes(n_tok, n_in) + 2 * pitch_bytes(n_out, n_in);
+}
+
+extern "C" size_t tcq_gated_ffn_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
+  if (check_sizes(n_tok, n_out, n_in, kMost) != TCQ_OK) return 0;
+  return pitch_bytes(n_tok, 2 * n_in) + 2 * pitch_bytes(n_out, 2 * n_in);
+}
+
+// dg and du; x, Wg and Wu where their rows need an aligned pitch
 extern "C" size_t tcq_gated_ffn_backward_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
-  if (check_sizes(n_tok, n_out, n_in, (1ll << 30) - 1) != TCQ_OK) return 0;
-  return 2 * (((size_t)n_tok * n_out * 2 + 255) & ~(size_t)255);
+  if (check_sizes(n_tok, n_out, n_in, kMost) != TCQ_OK) return 0;
+  return 2 * round256((size_t)n_tok * round_up(2 * n_out, 16)) + pitch_bytes(n_tok, 2 * n_in) +
+         2 * pitch_bytes(n_out, 2 * n_in);
+}
+
+static bool no_workspace(const void *ws, size_t have, size_t need) {
+  return need && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || have < need);
+}
+
+// a x w0^T (and a x w1^T) on operands of `es` bytes.
+template <bool I8, bool DUAL>
+static tcq_status_t product(const void *a, const void *w0, const void *w1, int es, int bf16, int64_t M, int64_t N,
+                            int64_t K, void *out, Epilogue e, void *ws, cudaStream_t s) {
+  Workspace w = {(char *)ws};
+  PairParams p;
+  p.shares = 0;
+  p.bf16 = bf16;
+  p.e = e;
+  Job &j = p.job[0];
+  Operand A, B;
+  tcq_status_t st = ready(A, a, M, K, es, w, s);
+  if (st != TCQ_OK) return st;
+  if (!map_of(&j.a[0], A, 128)) return TCQ_ERR_CUDA;
+  for (int i = 0; i < (DUAL ? 2 : 1); ++i) {
+    st = ready(B, i ? w1 : w0, N, K, es, w, s);
+    if (st != TCQ_OK) return st;
+    if (!map_of(&j.b[i], B, 128)) return TCQ_ERR_CUDA;
+  }
+  j.out[0] = out;
+  j.M = M;
+  j.N = N;
+  j.mt = (int)tiles(M, 256);
+  j.nt = (int)tiles(N, DUAL ? 128 : 256);
+  j.kb = (int)tiles(K * es, 128);
+  j.segs = 1;
+  j.z = 1;
+  j.a_mn = j.b_mn = 0;
+  j.wide = width(out, N, type_size(e.dtype));
+  return launch_pair<I8, DUAL>(p, s);
 }
 
 extern "C" tcq_status_t tcq_int8_matmul(const int8_t *a, const float *a_scale, const int8_t *w, const float *w_scale,
                                         const float *bias, int64_t n_tok, int64_t n_out, int64_t n_in, void *out,
                                         int out_dtype, void *ws, size_t ws_bytes, void *stream) {
-  if (out_dtype != TCQ_F16 && out_dtype != TCQ_BF16 && out_dtype != TCQ_F32) return TCQ_ERR_INVALID_ARG;
-  tcq_status_t st = check_sizes(n_tok, n_out, n_in, 131071);
+  if (bad_type(out_dtype)) return TCQ_ERR_INVALID_ARG;
+  tcq_status_t st = check_sizes(n_tok, n_out, n_in, kMostIn8);
   if (st != TCQ_OK) return st;
   if (n_tok == 0) return TCQ_OK;
   if (bad_ptr(a) || bad_ptr(a_scale) || bad_ptr(w) || bad_ptr(w_scale) || bad_ptr(out) || !aligned16(bias))
     return TCQ_ERR_INVALID_ARG;
-  Out o = {out, out_dtype, 0, a_scale, w_scale, nullptr, bias, nullptr, nullptr};
-  Operand<int8_t> A = {a, n_in, 1}, W = {w, n_in, 1}, none = {nullptr, 0, 0};
-  return run_product<int8_t, false>(A, W, none, none, n_tok, n_out, n_in, o, (cudaStream_t)stream);
+  if (no_workspace(ws, ws_bytes, tcq_int8_matmul_workspace_size(n_tok, n_out, n_in))) return TCQ_ERR_WORKSPACE;
+  const Epilogue e = {out_dtype, 0, a_scale, w_scale, nullptr, bias, nullptr, nullptr, 0};
+  return product<true, false>(a, w, nullptr, 1, 0, n_tok, n_out, n_in, out, e, ws, (cudaStream_t)stream);
 }
 
 extern "C" tcq_status_t tcq_int8_gated_ffn(const int8_t *a, const float *a_scale, const int8_t *w_gate,
                                            const float *w_gate_scale, const int8_t *w_up, const float *w_up_scale,
                                            int64_t n_tok, int64_t n_out, int64_t n_in, int act, void *h, int out_dtype,
                                            void *ws, size_t ws_bytes, void *stream) {
-  if (out_dtype != TCQ_F16 && out_dtype != TCQ_BF16 && out_dtype != TCQ_F32) return TCQ_ERR_INVALID_ARG;
-  if (act < TCQ_ACT_SILU || act > TCQ_ACT_RELU) return TCQ_ERR_INVALID_ARG;
-  tcq_status_t st = check_sizes(n_tok, n_out, n_in, 131071);
+  if (bad_type(out_dtype) || bad_act(act)) return TCQ_ERR_INVALID_ARG;
+  tcq_status_t st = check_sizes(n_tok, n_out, n_in, kMostIn8);
   if (st != TCQ_OK) return st;
   if (n_tok == 0) return TCQ_OK;
   if (bad_ptr(a) || bad_ptr(a_scale) || bad_ptr(w_gate) || bad_ptr(w_gate_scale) || bad_ptr(w_up) ||
       bad_ptr(w_up_scale) || bad_ptr(h))
     return TCQ_ERR_INVALID_ARG;
-  Out o = {h, out_dtype, act, a_scale, w_gate_scale, w_up_scale, nullptr, nullptr, nullptr};
-  Operand<int8_t> A = {a, n_in, 1}, G = {w_gate, n_in, 1}, U = {w_up, n_in, 1};
-  return run_product<int8_t, true>(A, G, A, U, n_tok, n_out, n_in, o, (cudaStream_t)stream);
-}
-
-template <typename T>
-static tcq_status_t gated(const void *x, const void *wg, const void *wu, int dtype, int64_t M, int64_t F, int64_t K,
-                          int act, void *h, float *gate, float *up, cudaStream_t s) {
-  Out o = {h, dtype, act, nullptr, nullptr, nullptr, nullptr, gate, up};
-  Operand<T> X = {(const T *)x, K, 1}, G = {(const T *)wg, K, 1}, U = {(const T *)wu, K, 1};
-  return run_product<T, true>(X, G, X, U, M, F, K, o, s);
+  if (no_workspace(ws, ws_bytes, tcq_int8_gated_ffn_workspace_size(n_tok, n_out, n_in))) return TCQ_ERR_WORKSPACE;
+  const Epilogue e = {out_dtype, act, a_scale, w_gate_scale, w_up_scale, nullptr, nullptr, nullptr, 0};
+  return product<true, true>(a, w_gate, w_up, 1, 0, n_tok, n_out, n_in, h, e, ws, (cudaStream_t)stream);
 }
 
 extern "C" tcq_status_t tcq_gated_ffn(const void *x, const void *w_gate, const void *w_up, int dtype, int64_t n_tok,
                                       int64_t n_out, int64_t n_in, int act, void *h, float *gate, float *up, void *ws,
                                       size_t ws_bytes, void *stream) {
-  if (dtype != TCQ_F16 && dtype != TCQ_BF16) return TCQ_ERR_INVALID_ARG;
-  if (act < TCQ_ACT_SILU || act > TCQ_ACT_RELU) return TCQ_ERR_INVALID_ARG;
-  tcq_status_t st = check_sizes(n_tok, n_out, n_in, (1ll << 30) - 1);
+  if ((dtype != TCQ_F16 && dtype != TCQ_BF16) || bad_act(act)) return TCQ_ERR_INVALID_ARG;
+  tcq_status_t st = check_sizes(n_tok, n_out, n_in, kMost);
   if (st != TCQ_OK) return st;
   if (!gate != !up) return TCQ_ERR_INVALID_ARG;
   if (n_tok == 0) return TCQ_OK;
   if (bad_ptr(x) || bad_ptr(w_gate) || bad_ptr(w_up) || bad_ptr(h) || !aligned16(gate) || !aligned16(up))
     return TCQ_ERR_INVALID_ARG;
-  cudaStream_t s = (cudaStream_t)stream;
-  return dtype == TCQ_F16 ? gated<__half>(x, w_gate, w_up, dtype, n_tok, n_out, n_in, act, h, gate, up, s)
-                          : gated<__nv_bfloat16>(x, w_gate, w_up, dtype, n_tok, n_out, n_in, act, h, gate, up, s);
-}
-
-template <typename T>
-static tcq_status_t gated_backward(const void *x, const void *wg, const void *wu, const float *gate, const float *up,
-                                   const void *grad, int dtype, int64_t M, int64_t F, int64_t K, int act, void *gx,
-                                   void *gwg, void *gwu, void *ws, cudaStream_t s) {
-  T *dg = (T *)ws;
-  T *du = (T *)((char *)ws + (((size_t)M * F * 2 + 255) & ~(size_t)255));
-  const int64_t n = M * F;
-  gate_grad_kernel<T><<<(unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sm_count() * 16), 256, 0, s>>>(
-      (const T *)grad, gate, up, n, act, dg, du);
-  tcq_status_t st = launch_status();
-  if (st != TCQ_OK) return st;
-  Out o = {nullptr, dtype, 0, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
-  const Operand<T> none = {nullptr, 0, 0};
-  if (gx) {
-    o.out = gx;
-    Operand<T> A = {dg, F, 1}, B = {(const T *)wg, 1, K}, A2 = {du, F, 1}, B2 = {(const T *)wu, 1, K};
-    st = run_product<T, false>(A, B, A2, B2, M, K, F, o, s);
-  }
-  for (int i = 0; i < 2 && st == TCQ_OK; ++i) {
-    o.out = i ? gwu : gwg;
-    if (!o.out) continue;
-    Operand<T> A = {i ? du : dg, 1, F}, B = {(const T *)x, 1, K};
-    st = run_product<T, false>(A, B, none, none, F, K, M, o, s);
-  }
-  return st;
+  if (no_workspace(ws, ws_bytes, tcq_gated_ffn_workspace_size(n_tok, n_out, n_in))) return TCQ_ERR_WORKSPACE;
+  Epilogue e = {dtype, act, nullptr, nullptr, nullptr, nullptr, gate, up, 0};
+  e.wide_save = std::min(width(gate, n_out, 4), width(up, n_out, 4));
+  return product<false, true>(x, w_gate, w_up, 2, dtype == TCQ_BF16, n_tok, n_out, n_in, h, e, ws,
+                              (cudaStream_t)stream);
 }
 
 extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, const float *gate,
                                                const float *up, const void *grad_h, int dtype, int64_t n_tok,
                                                int64_t n_out, int64_t n_in, int act, void *grad_x, void *grad_w_gate,
                                                void *grad_w_up, void *ws, size_t ws_bytes, void *stream) {
-  if (dtype != TCQ_F16 && dtype != TCQ_BF16) return TCQ_ERR_INVALID_ARG;
-  if (act < TCQ_ACT_SILU || act > TCQ_ACT_RELU) return TCQ_ERR_INVALID_ARG;
-  tcq_status_t st = check_sizes(n_tok, n_out, n_in, (1ll << 30) - 1);
+  if ((dtype != TCQ_F16 && dtype != TCQ_BF16) || bad_act(act)) return TCQ_ERR_INVALID_ARG;
+  tcq_status_t st = check_sizes(n_tok, n_out, n_in, kMost);
   if (st != TCQ_OK) return st;
   if (!aligned16(grad_x) || !aligned16(grad_w_gate) || !aligned16(grad_w_up)) return TCQ_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
-  if (n_tok == 0) {                                   // no token: the weights' gradients are zero
+  if (n_tok == 0) {                                      // no token: the weights' gradients are zero
     for (void *g : {grad_w_gate, grad_w_up})
       if (g && cudaMemsetAsync(g, 0, (size_t)n_out * n_in * 2, s) != cudaSuccess) return TCQ_ERR_CUDA;
     return TCQ_OK;
@@ -231,10 +616,72 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
   if (bad_ptr(x) || bad_ptr(w_gate) || bad_ptr(w_up) || bad_ptr(gate) || bad_ptr(up) || bad_ptr(grad_h))
     return TCQ_ERR_INVALID_ARG;
   if (!grad_x && !grad_w_gate && !grad_w_up) return TCQ_OK;
-  if (!ws || !aligned256(ws) || ws_bytes < tcq_gated_ffn_backward_workspace_size(n_tok, n_out, n_in))
-    return TCQ_ERR_WORKSPACE;
-  return dtype == TCQ_F16 ? gated_backward<__half>(x, w_gate, w_up, gate, up, grad_h, dtype, n_tok, n_out, n_in, act,
-                                                   grad_x, grad_w_gate, grad_w_up, ws, s)
-                          : gated_backward<__nv_bfloat16>(x, w_gate, w_up, gate, up, grad_h, dtype, n_tok, n_out, n_in,
-                                                          act, grad_x, grad_w_gate, grad_w_up, ws, s);
+  if (no_workspace(ws, ws_bytes, tcq_gated_ffn_backward_workspace_size(n_tok, n_out, n_in))) return TCQ_ERR_WORKSPACE;
+
+  Workspace w = {(char *)ws};
+  const int64_t pitch = round_up(2 * n_out, 16);
+  Operand d[2], X, W[2];
+  for (Operand &o : d) o = {w.take((size_t)n_tok * pitch), n_tok, n_out, pitch, 2};
+  const unsigned blocks = blocks_for(n_tok * n_out);
+  if (dtype == TCQ_F16)
+    gate_grad_kernel<<<blocks, 256, 0, s>>>((const __half *)grad_h, gate, up, n_tok, n_out, pitch / 2, act,
+                                            (__half *)d[0].p, (__half *)d[1].p);
+  else
+    gate_grad_kernel<<<blocks, 256, 0, s>>>((const __nv_bfloat16 *)grad_h, gate, up, n_tok, n_out, pitch / 2, act,
+                                            (__nv_bfloat16 *)d[0].p, (__nv_bfloat16 *)d[1].p);
+  st = launch_status();
+  if (st != TCQ_OK) return st;
+
+  PairParams p;
+  p.bf16 = dtype == TCQ_BF16;
+  p.e = {dtype, 0, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0};
+  Job &j = p.job[0];
+  if (grad_x) {
+    // one sum over both halves: dg Wg, then du Wu; the weights' rows run along it
+    for (int i = 0; i < 2; ++i) {
+      st = ready(W[i], i ? w_up : w_gate, n_out, n_in, 2, w, s);
+      if (st != TCQ_OK) return st;
+      if (!map_of(&j.a[i], d[i], 128) || !map_of(&j.b[i], W[i], 64)) return TCQ_ERR_CUDA;
+    }
+    j.out[0] = grad_x;
+    j.M = n_tok;
+    j.N = n_in;
+    j.mt = (int)tiles(n_tok, 256);
+    j.nt = (int)tiles(n_in, 256);
+    j.kb = (int)tiles(n_out, 64);
+    j.segs = 2;
+    j.z = 1;
+    j.a_mn = 0;
+    j.b_mn = 1;
+    j.wide = width(grad_x, n_in, 2);
+    p.shares = 0;
+    st = launch_pair<false, false>(p, s);
+    if (st != TCQ_OK) return st;
+  }
+  if (grad_w_gate || grad_w_up) {
+    // dg^T x and du^T x: both operands' rows (tokens) run along the sum
+    st = ready(X, x, n_tok, n_in, 2, w, s);
+    if (st != TCQ_OK) return st;
+    if (!map_of(&j.b[0], X, 64)) return TCQ_ERR_CUDA;
+    int z = 0;
+    j.wide = 32;
+    for (int i = 0; i < 2; ++i) {
+      void *g = i ? grad_w_up : grad_w_gate;
+      if (!g) continue;
+      if (!map_of(&j.a[z], d[i], 64)) return TCQ_ERR_CUDA;
+      j.out[z++] = g;
+      j.wide = std::min(j.wide, width(g, n_in, 2));
+    }
+    j.M = n_out;
+    j.N = n_in;
+    j.mt = (int)tiles(n_out, 256);
+    j.nt = (int)tiles(n_in, 256);
+    j.kb = (int)tiles(n_tok, 64);
+    j.segs = 1;
+    j.z = z;
+    j.a_mn = j.b_mn = 1;
+    p.shares = 0;
+    st = launch_pair<false, false>(p, s);
+  }
+  return st;
 }
