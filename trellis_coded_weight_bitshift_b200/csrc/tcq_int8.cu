@@ -7,94 +7,232 @@
 // about half of scale), and |r| against scale / 2 says whether q0 stays.
 // Rows below 2^-60 are first multiplied by 2^64 (exact), so that neither
 // 1 / scale nor scale / 2 leaves the normal range.
+//   A row is read once: up to 4,096 bytes by one warp, up to 16,384 by a block,
+// into registers (16 bytes a load), its largest value is found, and it is
+// written; longer rows are read a second time.  Bound by HBM traffic, then by
+// issue: about five instructions a value (conversion, one fma, one subtraction,
+// one fma and a maximum for the check, byte packing; pairs where the hardware
+// has them).  Only where the check of eight values fails are they decided one by
+// one: a value lies that close to a border about once in 10^5.
 //
 // decode_int8: the 1MAD code is (bytesum - 510) / 147.8 [QTIP blog, "The
 // codebook is computed"]; its numerator is a whole number of at most 483 in
-// size at L = 8, 12 and 16, and a quarter of it fits 8 bits.
+// size at L = 8, 12 and 16, and a quarter of it fits 8 bits.  The byte sum is
+// taken into the mantissa of 2^21 + (sum + 514) / 4 (an ulp of 1/4), and adding
+// 1.5 * 2^23 - 2^21 - 256 rounds the quarter to nearest even and leaves q in
+// the low byte: two instructions for sum, centring, division and rounding.
 #include <algorithm>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "tcq_device.cuh"
 
 namespace tcq {
 
-template <typename T> __device__ __forceinline__ float to_f32(T v);
-template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+constexpr float kRound = 12582912.0f;                   // 1.5 * 2^23: adding it rounds to a whole number
 
-struct RowScale {
-  float up;      // 1 or 2^64: what x is multiplied by first
-  float scale;   // of the multiplied row
-  float inv, half;
-};
-
-// x / scale to the nearest integer, ties to even, as the low byte of the
-// result's bits (1.5 * 2^23 + q keeps q in two's complement there).
-__device__ __forceinline__ uint32_t quantize_one(float x, const RowScale &s) {
-  constexpr float kMagic = 12582912.0f;
-  x *= s.up;
-  float u = __fadd_rn(__fmul_rn(x, s.inv), kMagic);
-  const float q = __fsub_rn(u, kMagic);
-  const float r = __fmaf_rn(-q, s.scale, x);
-  if (fabsf(r) >= s.half) {
-    const bool odd = __float_as_uint(u) & 1u;
-    if (fabsf(r) > s.half || odd) u = __fadd_rn(u, copysignf(1.0f, r));
-  }
+// x / scale to the nearest integer, ties to even, in the low byte of the
+// result's bits (kRound + q keeps q in two's complement there).
+__device__ __forceinline__ uint32_t quantize_exactly(float x, float scale, float inv) {
+  float u = __fmaf_rn(x, inv, kRound);
+  const float r = __fmaf_rn(-__fsub_rn(u, kRound), scale, x), half = 0.5f * scale;
+  if (fabsf(r) > half || (fabsf(r) == half && (__float_as_uint(u) & 1u))) u = __fadd_rn(u, copysignf(1.0f, r));
   return __float_as_uint(u);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, int64_t cols,
-                                                            int8_t *__restrict__ q,
-                                                            float *__restrict__ scale) {
-  __shared__ uint32_t part[8];
-  const T *row = x + (int64_t)blockIdx.x * cols;
-  uint32_t top = 0;                                   // bits of the largest |x|; a NaN is above infinity
-  for (int64_t i = threadIdx.x; i < cols; i += 256)
-    top = max(top, __float_as_uint(to_f32<T>(row[i])) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
-  __syncthreads();
-  top = 0;
-  for (int w = 0; w < 8; ++w) top = max(top, part[w]);
-  const float amax = __uint_as_float(top);
-  const float sc = __fdiv_rn(amax, 127.0f);
-  if (threadIdx.x == 0) scale[blockIdx.x] = top < 0x7F800000u ? sc : __uint_as_float(0x7FC00000u);
-  int8_t *out = q + (int64_t)blockIdx.x * cols;
-  if (top >= 0x7F800000u || sc == 0.0f) {
-    for (int64_t i = threadIdx.x; i < cols; i += 256) out[i] = 0;
-    return;
+// N values (1, 4 or 8) of one thread, as they are loaded: raw words of type T.
+template <typename T, int N> struct Values {
+  static constexpr int kWords = (N * (int)sizeof(T) + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T *p) {
+    if (N == 1) {
+      w[0] = sizeof(T) == 4 ? __ldg(reinterpret_cast<const uint32_t *>(p))
+                            : __ldg(reinterpret_cast<const unsigned short *>(p));
+    } else {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+      w[0] = v.x; w[1 % kWords] = v.y; w[2 % kWords] = v.z; w[3 % kWords] = v.w;
+    }
   }
-  RowScale s;
-  s.up = amax < 0x1p-60f ? 0x1p64f : 1.0f;
-  s.scale = sc * s.up;
-  s.inv = 1.0f / s.scale;
-  s.half = 0.5f * s.scale;
-  for (int64_t i = threadIdx.x; i < cols; i += 256) out[i] = (int8_t)quantize_one(to_f32<T>(row[i]), s);
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // The largest |value|'s bits so far (16-bit types: one maximum for each half of the word).
+  __device__ __forceinline__ uint32_t top(uint32_t t) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      t = sizeof(T) == 4 ? max(t, w[i] & 0x7FFFFFFFu) : __vmaxu2(t, w[i] & 0x7FFF7FFFu);
+    return t;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if (sizeof(T) == 4) return __uint_as_float(w[i % kWords]);
+    const uint32_t h = w[(i >> 1) % kWords];
+    if (std::is_same<T, __half>::value)
+      return __half2float(__ushort_as_half((unsigned short)((i & 1) ? h >> 16 : h)));
+    return __uint_as_float((i & 1) ? h & 0xFFFF0000u : h << 16);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t top_as_f32(uint32_t t) {
+  if (sizeof(T) == 4) return t;
+  const unsigned short h = (unsigned short)max(t & 0xFFFFu, t >> 16);
+  return std::is_same<T, __half>::value ? __float_as_uint(__half2float(__ushort_as_half(h))) : (uint32_t)h << 16;
 }
 
-// One thread per weight.
+template <typename T, int N>
+__device__ __forceinline__ void quantize_store(const Values<T, N> &v, float up, float scale, float inv, int8_t *q) {
+  float x[N], worst = 0.0f;
+  uint32_t u[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = v.get(i) * up;
+  if (N == 1) {
+    q[0] = (int8_t)quantize_exactly(x[0], scale, inv);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const f2_t xx = f2(x[2 * i], x[(2 * i + 1) % N]);
+    const f2_t uu = f2fma(xx, f2(inv, inv), f2(kRound, kRound));
+    const f2_t rr = f2fma(f2sub(f2(kRound, kRound), uu), f2(scale, scale), xx);
+    worst = fmaxf(worst, fmaxf(fabsf(f2lo(rr)), fabsf(f2hi(rr))));
+    u[2 * i] = __float_as_uint(f2lo(uu));
+    u[(2 * i + 1) % N] = __float_as_uint(f2hi(uu));
+  }
+  if (worst >= 0.5f * scale) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = quantize_exactly(x[i], scale, inv);
+  }
+  uint32_t b[(N + 3) / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    b[i] = __byte_perm(__byte_perm(u[4 * i], u[(4 * i + 1) % N], 0x0040), __byte_perm(u[(4 * i + 2) % N], u[(4 * i + 3) % N], 0x0040),
+                       0x5410);
+  if (N == 4) *reinterpret_cast<uint32_t *>(q) = b[0];
+  else *reinterpret_cast<uint2 *>(q) = make_uint2(b[0], b[(N + 3) / 4 - 1]);
+}
+
+// One row by TPR threads (32 or 256 of the block's 256), KEEP loads of N values
+// a thread kept in registers; what a longer row has beyond them is read twice.
+template <typename T, int N, int TPR, int KEEP>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
+                                                            int8_t *__restrict__ q, float *__restrict__ scale) {
+  __shared__ uint32_t part[8];
+  const int t = threadIdx.x % TPR;
+  const int64_t r = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  if (TPR == 32 && r >= rows) return;                   // whole warps: no block barrier follows
+  const T *row = x + r * cols;
+  int8_t *out = q + r * cols;
+  Values<T, N> v[KEEP], w;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int64_t c = ((int64_t)i * TPR + t) * N;
+    if (c < cols) v[i].load(row + c);
+    else v[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) top = v[i].top(top);
+  for (int64_t c = ((int64_t)KEEP * TPR + t) * N; c < cols; c += (int64_t)TPR * N) {
+    w.load(row + c);
+    top = w.top(top);
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top_as_f32<T>(top));
+  if (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xFFFFFFFFu, part[threadIdx.x & 7]);
+  }
+  // an infinity or NaN in the row: a NaN scale and zeros; no scale: zeros (x * 0 = 0 for every finite x)
+  const float amax = __uint_as_float(top), sc = __fdiv_rn(amax, 127.0f);
+  const bool fine = top < 0x7F800000u;
+  if (t == 0) scale[r] = fine ? sc : __uint_as_float(0x7FC00000u);
+  float up = amax < 0x1p-60f ? 0x1p64f : 1.0f;
+  const float by = sc * up;
+  const float inv = fine && by > 0.0f ? 1.0f / by : 0.0f;
+  if (!(inv > 0.0f)) {
+    for (int64_t c = t; c < cols; c += TPR) out[c] = 0;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int64_t c = ((int64_t)i * TPR + t) * N;
+    if (c < cols) quantize_store<T, N>(v[i], up, by, inv, out + c);
+  }
+  for (int64_t c = ((int64_t)KEEP * TPR + t) * N; c < cols; c += (int64_t)TPR * N) {
+    w.load(row + c);
+    quantize_store<T, N>(w, up, by, inv, out + c);
+  }
+}
+
+// The state's quarter numerator in the low byte (the comment at the top).
+__device__ __forceinline__ uint32_t quarter_code(uint32_t state) {
+  const uint32_t m = __dp4a(state * kLcgMul + kLcgAdd, 0x01010101u, 0x4A000000u + 514u);
+  return __float_as_uint(__fadd_rn(__uint_as_float(m), 12582912.0f - 2097152.0f - 256.0f));
+}
+
+// The sixteen weights whose windows start in word `hi`.
 template <int L>
-__global__ void __launch_bounds__(256) decode_int8_kernel(const uint32_t *__restrict__ bits,
-                                                          int64_t n_weights, int T, int layout,
-                                                          int wps, int tiles_c, int8_t *__restrict__ out) {
-  for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < n_weights;
-       g += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t seq = g / T;
-    const int t = (int)(g - seq * T);
-    const uint32_t *src = bits + seq * wps;
-    const int i = t >> 4, o = 2 * (t & 15);
-    const int i1 = i + 1 < wps ? i + 1 : 0;
-    const uint32_t lo = i + 1 < wps || layout == TCQ_TAILBITING ? src[i1] : 0u;
-    const uint32_t state = __funnelshift_l(lo, src[i], o) >> (32 - L);
-    const int k = (int)one_mad_bytesum(state) - 510;
-    int64_t at = g;
-    if (tiles_c > 0) {
-      const int64_t tr = seq / tiles_c, tc = seq - tr * tiles_c;
-      at = (tr * 16 + (t >> 4)) * ((int64_t)tiles_c * 16) + tc * 16 + (t & 15);
+__device__ __forceinline__ uint4 decode16(uint32_t hi, uint32_t lo) {
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = quarter_code(__funnelshift_l(lo, hi, 8 * i + 2 * j) >> (32 - L));
+    b[i] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+  }
+  return make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+// One thread per 16 x 16 tile: its stream in registers, a row of it in one
+// 16-byte store; a warp's stores cover 512 neighbouring bytes.
+template <int L, int LAYOUT>
+__global__ void __launch_bounds__(128) decode_int8_tiles_kernel(const uint32_t *__restrict__ bits, int64_t n_seq,
+                                                                int tiles_c, int wps, int8_t *__restrict__ out) {
+  const int64_t seq = (int64_t)blockIdx.x * 128 + threadIdx.x;
+  if (seq >= n_seq) return;
+  const uint32_t *src = bits + seq * wps;
+  uint32_t w[17];
+  if (LAYOUT == TCQ_TAILBITING) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
     }
-    out[at] = (int8_t)__float2int_rn(0.25f * (float)k);
+    w[16] = w[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 17; ++i) w[i] = __ldg(src + i);
+  }
+  const int64_t tr = seq / tiles_c, tc = seq - tr * tiles_c, cols = (int64_t)tiles_c * 16;
+  int8_t *dst = out + tr * 16 * cols + tc * 16;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) *reinterpret_cast<uint4 *>(dst + r * cols) = decode16<L>(w[r], w[r + 1]);
+}
+
+// One thread per word of the stream, sixteen weights in sequence order (T a
+// multiple of 16: one 16-byte store), the last word's fewer.
+template <int L>
+__global__ void __launch_bounds__(256) decode_int8_seq_kernel(const uint32_t *__restrict__ bits, int64_t n_items,
+                                                              int per_seq, int T, int layout, int wps,
+                                                              int8_t *__restrict__ out) {
+  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < n_items; g += (int64_t)gridDim.x * 256) {
+    const int64_t seq = g / per_seq;
+    const int i = (int)(g - seq * per_seq);
+    const uint32_t *src = bits + seq * wps;
+    const uint32_t lo = i + 1 < wps ? __ldg(src + i + 1) : layout == TCQ_TAILBITING ? __ldg(src) : 0u;
+    const uint4 v = decode16<L>(__ldg(src + i), lo);
+    int8_t *dst = out + seq * T + 16 * i;
+    if (T % 16 == 0) {
+      *reinterpret_cast<uint4 *>(dst) = v;
+    } else {
+      const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+      const int n = min(16, T - 16 * i);
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k < n) dst[k] = (int8_t)(b[k >> 2] >> (8 * (k & 3)));
+    }
   }
 }
 
@@ -105,6 +243,29 @@ using namespace tcq_host;
 
 static bool size_ok(int64_t n) { return n < (1ll << 30); }
 
+template <typename T, int N, int TPR, int KEEP>
+static tcq_status_t quantize_launch(const T *x, int64_t rows, int64_t cols, int8_t *q, float *scale, cudaStream_t s) {
+  const unsigned blocks = (unsigned)((rows + 256 / TPR - 1) / (256 / TPR));
+  quantize_rows_kernel<T, N, TPR, KEEP><<<blocks, 256, 0, s>>>(x, rows, cols, q, scale);
+  return launch_status();
+}
+
+// Whole 16-byte loads where every row starts on such a boundary; a warp a row
+// while the row fits its registers, else a block.
+template <typename T>
+static tcq_status_t quantize_any(const T *x, int64_t rows, int64_t cols, int8_t *q, float *scale, cudaStream_t s) {
+  constexpr int N = 16 / (int)sizeof(T);
+  if (cols % N) {
+    if (cols <= 256) return quantize_launch<T, 1, 32, 8>(x, rows, cols, q, scale, s);
+    return quantize_launch<T, 1, 256, 8>(x, rows, cols, q, scale, s);
+  }
+  const int64_t loads = cols / N;
+  if (loads <= 64) return quantize_launch<T, N, 32, 2>(x, rows, cols, q, scale, s);
+  if (loads <= 256) return quantize_launch<T, N, 32, 8>(x, rows, cols, q, scale, s);
+  if (loads <= 512) return quantize_launch<T, N, 256, 2>(x, rows, cols, q, scale, s);
+  return quantize_launch<T, N, 256, 4>(x, rows, cols, q, scale, s);
+}
+
 extern "C" tcq_status_t tcq_quantize_int8(const void *x, int dtype, int64_t rows, int64_t cols, int8_t *q,
                                           float *scale, void *stream) {
   if (dtype != TCQ_F16 && dtype != TCQ_BF16 && dtype != TCQ_F32) return TCQ_ERR_INVALID_ARG;
@@ -113,13 +274,26 @@ extern "C" tcq_status_t tcq_quantize_int8(const void *x, int dtype, int64_t rows
   if (rows == 0) return TCQ_OK;
   if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale)) return TCQ_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
-  const unsigned blocks = (unsigned)rows;
-  if (dtype == TCQ_F16)
-    quantize_rows_kernel<<<blocks, 256, 0, s>>>((const __half *)x, cols, q, scale);
-  else if (dtype == TCQ_BF16)
-    quantize_rows_kernel<<<blocks, 256, 0, s>>>((const __nv_bfloat16 *)x, cols, q, scale);
-  else
-    quantize_rows_kernel<<<blocks, 256, 0, s>>>((const float *)x, cols, q, scale);
+  if (dtype == TCQ_F16) return quantize_any((const __half *)x, rows, cols, q, scale, s);
+  if (dtype == TCQ_BF16) return quantize_any((const __nv_bfloat16 *)x, rows, cols, q, scale, s);
+  return quantize_any((const float *)x, rows, cols, q, scale, s);
+}
+
+template <int L>
+static tcq_status_t decode_launch(const tcq_trellis_t *tr, const uint32_t *bits, int64_t n_seq, int layout,
+                                  int64_t cols, int8_t *out, int wps, cudaStream_t s) {
+  if (cols) {
+    const unsigned blocks = (unsigned)((n_seq + 127) / 128);
+    if (layout == TCQ_TAILBITING)
+      decode_int8_tiles_kernel<L, TCQ_TAILBITING><<<blocks, 128, 0, s>>>(bits, n_seq, (int)(cols / 16), wps, out);
+    else
+      decode_int8_tiles_kernel<L, TCQ_FREE_START><<<blocks, 128, 0, s>>>(bits, n_seq, (int)(cols / 16), wps, out);
+  } else {
+    const int per_seq = (tr->seq_len + 15) / 16;
+    const int64_t n = n_seq * per_seq;
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 30);
+    decode_int8_seq_kernel<L><<<blocks, 256, 0, s>>>(bits, n, per_seq, tr->seq_len, layout, wps, out);
+  }
   return launch_status();
 }
 
@@ -138,17 +312,14 @@ extern "C" tcq_status_t tcq_decode_int8(const tcq_trellis_t *tr, const uint32_t 
     if (rows <= 0 || cols <= 0 || rows % 16 || cols % 16) return TCQ_ERR_INVALID_ARG;
     if (!size_ok(rows) || !size_ok(cols)) return TCQ_ERR_UNSUPPORTED;
     if ((rows / 16) * (cols / 16) != n_seq) return TCQ_ERR_INVALID_ARG;
+    if (n_seq > (1ll << 37)) return TCQ_ERR_UNSUPPORTED;     // blocks of 128 tiles: a grid's most
   }
   if (n_seq == 0) return TCQ_OK;
   if (!bits || !out || !aligned16(bits) || !aligned16(out)) return TCQ_ERR_INVALID_ARG;
-  const int64_t nw = n_seq * tr->seq_len;
-  const unsigned blocks = (unsigned)std::min<int64_t>((nw + 255) / 256, (int64_t)sm_count() * 32);
-  const int tc = tiles ? (int)(cols / 16) : 0;
   cudaStream_t s = (cudaStream_t)stream;
   switch (tr->L) {
-    case 8: decode_int8_kernel<8><<<blocks, 256, 0, s>>>(bits, nw, tr->seq_len, layout, (int)wps, tc, out); break;
-    case 12: decode_int8_kernel<12><<<blocks, 256, 0, s>>>(bits, nw, tr->seq_len, layout, (int)wps, tc, out); break;
-    default: decode_int8_kernel<16><<<blocks, 256, 0, s>>>(bits, nw, tr->seq_len, layout, (int)wps, tc, out); break;
+    case 8: return decode_launch<8>(tr, bits, n_seq, layout, tiles ? cols : 0, out, (int)wps, s);
+    case 12: return decode_launch<12>(tr, bits, n_seq, layout, tiles ? cols : 0, out, (int)wps, s);
+    default: return decode_launch<16>(tr, bits, n_seq, layout, tiles ? cols : 0, out, (int)wps, s);
   }
-  return launch_status();
 }
