@@ -340,6 +340,189 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0 && stop) atomicAdd(&g_gave_up, 1u);
 }
 
+// ---- few tokens: the weights on the M side
+struct RowsParams {
+  CUtensorMap w[2], x;
+  int64_t M, N;
+  int kb, bf16, wide4;
+  void *out;
+  Epilogue e;
+};
+
+template <bool DUAL, int NT> struct RowsShape {
+  static constexpr int kWeightBytes = DUAL ? 32768 : 16384, kStage = kWeightBytes + NT * 128;
+  // two blocks an SM where four stages and more fit twice (three of the dual ones), else one
+  static constexpr int kDepth = DUAL ? (NT <= 32 ? 3 : NT == 64 ? 5 : 4) : (NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3);
+  static constexpr int kBlocksPerSm = DUAL && NT >= 64 ? 1 : 2;
+  static constexpr int kCols = DUAL ? 2 * NT : NT, kTmem = kCols < 32 ? 32 : kCols;
+  static constexpr int kSmem = kDepth * kStage + 1024;
+  static_assert(kCols * 512 <= kDepth * kStage, "the partial sums reuse the ring");
+};
+
+__device__ __forceinline__ void add4(float4 &s, const float4 &v, bool i8) {
+  if (i8) {
+    s.x = __int_as_float(__float_as_int(s.x) + __float_as_int(v.x));
+    s.y = __int_as_float(__float_as_int(s.y) + __float_as_int(v.y));
+    s.z = __int_as_float(__float_as_int(s.z) + __float_as_int(v.z));
+    s.w = __int_as_float(__float_as_int(s.w) + __float_as_int(v.w));
+  } else {
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+}
+
+// A cluster works on 128 channels by NT tokens; its blocks split the
+// contraction and add their sums through distributed shared memory.
+template <bool I8, bool DUAL, int NT>
+__global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
+    rows_kernel(const __grid_constant__ RowsParams p) {
+  typedef RowsShape<DUAL, NT> Sh;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[2 * Sh::kDepth + 1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t stop;
+  const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * Sh::kDepth, acc_full = empty + 8 * Sh::kDepth;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = (int)cluster_size(), rank = (int)cluster_rank();
+  const int64_t n0 = (int64_t)(blockIdx.x / split) * 128, m0 = (int64_t)blockIdx.y * NT;
+  const int kb0 = (int)((int64_t)p.kb * rank / split), kb1 = (int)((int64_t)p.kb * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    stop = 0;
+    for (int i = 0; i < 2 * Sh::kDepth + 1; ++i) mbar_init(full + 8 * i, 1);
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, Sh::kTmem);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(empty + 8 * s, ph ^ 1, &stop)) { ok = false; break; }
+      const uint32_t at = ring + s * Sh::kStage, bar = full + 8 * s;
+      const int k = kb * (I8 ? 128 : 64);
+      mbar_expect(bar, Sh::kStage);
+      tma_load(at, &p.w[0], k, (int)n0, bar);
+      if (DUAL) tma_load(at + 16384, &p.w[1], k, (int)n0, bar);
+      tma_load(at + Sh::kWeightBytes, &p.x, k, (int)m0, bar);
+      if (++s == Sh::kDepth) { s = 0; ph ^= 1; }
+    }
+    if (!ok)                                             // gave up: the copies in flight land first
+      for (int i = 0; i < Sh::kDepth; ++i) {
+        s = s ? s - 1 : Sh::kDepth - 1;
+        if (s == Sh::kDepth - 1) ph ^= 1;
+        const unsigned long long t0 = now_ns();
+        while (!mbar_try(full + 8 * s, ph) && now_ns() - t0 < kWaitNs / 16) {}
+      }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t instr = I8 ? instr_i8(128, NT) : instr_f16(128, NT, p.bf16, 0, 0);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(full + 8 * s, ph, &stop)) break;
+      tmem_fence_after_sync();
+      const uint32_t at = ring + s * Sh::kStage;
+      const uint64_t w0 = operand_desc(at, false), w1 = operand_desc(at + 16384, false),
+                     x = operand_desc(at + Sh::kWeightBytes, false);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mma<I8, false>(tmem, w0 + 2 * i, x + 2 * i, instr, kb > kb0 || i > 0);
+        if (DUAL) mma<I8, false>(tmem + NT, w1 + 2 * i, x + 2 * i, instr, kb > kb0 || i > 0);
+      }
+      mma_commit(empty + 8 * s);
+      if (++s == Sh::kDepth) { s = 0; ph ^= 1; }
+    }
+    mma_commit(acc_full);
+  } else if (warp >= 2) {
+    // sums to shared memory, [column][channel]: the ring is free once all products are done
+    const int quarter = warp & 3;
+    const bool got = mbar_wait(acc_full, 0, &stop);
+    if (__all_sync(0xFFFFFFFFu, got)) {
+      tmem_fence_after_sync();
+      const int cols = (int)min((int64_t)NT, p.M - m0);
+      const uint32_t ch = ring + 4 * (quarter * 32 + lane);
+#pragma unroll 1
+      for (int c = 0; c < Sh::kCols; c += 16) {
+        const int left = cols - (c & (NT - 1));          // columns of tokens that exist
+        if (left <= 0) continue;
+        float v[16];
+        tmem_ld16(tmem + ((uint32_t)quarter << 21) + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < left)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(ch + 512 * (c + i)), "f"(v[i]) : "memory");
+      }
+    }
+  }
+  __syncwarp();
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
+  cluster_sync();
+
+  // each block finishes 128 / split of the channels, four a thread
+  const int quads = 32 / split, cols = (int)min((int64_t)NT, p.M - m0);
+  uint32_t peer[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) peer[r] = r < split ? map_to_rank(ring, r) : 0;
+  for (int i = threadIdx.x; i < quads * cols; i += 192) {
+    const int q = rank * quads + i % quads, c = i / quads;
+    const int64_t ch = n0 + 4 * q, row = m0 + c;
+    const int valid = (int)min((int64_t)4, p.N - ch);
+    if (valid <= 0) continue;
+    const uint32_t off = 512 * c + 16 * q;
+    float4 g = make_float4(0, 0, 0, 0), u = g;           // four zero bit patterns: int32 zeros too
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if (r >= split) break;
+      add4(g, ld_cluster4(peer[r] + off), I8);
+      if (DUAL) add4(u, ld_cluster4(peer[r] + off + 512 * NT), I8);
+    }
+    float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
+    const int64_t at = row * p.N + ch;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= valid) continue;
+      if (I8) {
+        const float sa = __ldg(p.e.a_scale + row);
+        gv[k] = (float)__float_as_int(gv[k]) * sa * __ldg(p.e.s0 + ch + k);
+        if (DUAL) uv[k] = (float)__float_as_int(uv[k]) * sa * __ldg(p.e.s1 + ch + k);
+        else if (p.e.bias) gv[k] = __fadd_rn(gv[k], __ldg(p.e.bias + ch + k));
+      }
+      if (DUAL) {
+        if (!I8 && p.e.gate) {
+          p.e.gate[at + k] = gv[k];
+          p.e.up[at + k] = uv[k];
+        }
+        gv[k] = activation(gv[k], p.e.act) * uv[k];
+      }
+    }
+    if (valid == 4 && p.wide4) {
+      if (p.e.dtype == TCQ_F32)
+        *reinterpret_cast<float4 *>((float *)p.out + at) = make_float4(gv[0], gv[1], gv[2], gv[3]);
+      else
+        *reinterpret_cast<uint2 *>((uint16_t *)p.out + at) =
+            make_uint2(pack2(gv[0], gv[1], p.e.dtype), pack2(gv[2], gv[3], p.e.dtype));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k >= valid) continue;
+        if (p.e.dtype == TCQ_F32) ((float *)p.out)[at + k] = gv[k];
+        else ((uint16_t *)p.out)[at + k] = (uint16_t)pack2(gv[k], 0.0f, p.e.dtype);
+      }
+    }
+  }
+  cluster_sync();                                        // no block leaves while its sums are read
+  if (threadIdx.x == 0 && stop) atomicAdd(&g_gave_up, 1u);
+}
+
 // Rows of `bytes` bytes, packed, to rows `pitch` bytes apart (a multiple of 16),
 // 16 bytes a thread.  The source is read in whole aligned words; the last row's
 // end is read by bytes, so nothing past it is touched.
@@ -487,6 +670,30 @@ tcq_status_t launch_pair(PairParams &p, cudaStream_t s) {
   return launch_status();
 }
 
+template <bool I8, bool DUAL, int NT>
+tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
+  typedef RowsShape<DUAL, NT> Sh;
+  if (cudaFuncSetAttribute(rows_kernel<I8, DUAL, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
+      cudaSuccess)
+    return TCQ_ERR_CUDA;
+  // split the contraction while the blocks still fit the GPU at once and each keeps four steps of it
+  const int64_t nt = tiles(p.N, 128), mt = tiles(p.M, NT), slots = (int64_t)sm_count() * Sh::kBlocksPerSm;
+  int split = 1;
+  while (split < 8 && 2 * split * nt * mt <= slots && p.kb >= 8 * split) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(nt * split), (unsigned)mt);
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rows_kernel<I8, DUAL, NT>, p) == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" tcq_status_t tcq_products_gave_up(unsigned int *count) {
@@ -525,20 +732,35 @@ template <bool I8, bool DUAL>
 static tcq_status_t product(const void *a, const void *w0, const void *w1, int es, int bf16, int64_t M, int64_t N,
                             int64_t K, void *out, Epilogue e, void *ws, cudaStream_t s) {
   Workspace w = {(char *)ws};
+  Operand A, B[2];
+  tcq_status_t st = ready(A, a, M, K, es, w, s);
+  for (int i = 0; i < (DUAL ? 2 : 1) && st == TCQ_OK; ++i) st = ready(B[i], i ? w1 : w0, N, K, es, w, s);
+  if (st != TCQ_OK) return st;
+  if (M <= 128) {
+    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    RowsParams r;
+    if (!map_of(&r.w[0], B[0], 128) || (DUAL && !map_of(&r.w[1], B[1], 128)) || !map_of(&r.x, A, nt))
+      return TCQ_ERR_CUDA;
+    r.M = M;
+    r.N = N;
+    r.kb = (int)tiles(K * es, 128);
+    r.bf16 = bf16;
+    r.wide4 = N % 4 == 0;
+    r.out = out;
+    r.e = e;
+    return nt == 16   ? launch_rows<I8, DUAL, 16>(r, s)
+           : nt == 32 ? launch_rows<I8, DUAL, 32>(r, s)
+           : nt == 64 ? launch_rows<I8, DUAL, 64>(r, s)
+                      : launch_rows<I8, DUAL, 128>(r, s);
+  }
   PairParams p;
   p.shares = 0;
   p.bf16 = bf16;
   p.e = e;
   Job &j = p.job[0];
-  Operand A, B;
-  tcq_status_t st = ready(A, a, M, K, es, w, s);
-  if (st != TCQ_OK) return st;
   if (!map_of(&j.a[0], A, 128)) return TCQ_ERR_CUDA;
-  for (int i = 0; i < (DUAL ? 2 : 1); ++i) {
-    st = ready(B, i ? w1 : w0, N, K, es, w, s);
-    if (st != TCQ_OK) return st;
-    if (!map_of(&j.b[i], B, 128)) return TCQ_ERR_CUDA;
-  }
+  for (int i = 0; i < (DUAL ? 2 : 1); ++i)
+    if (!map_of(&j.b[i], B[i], 128)) return TCQ_ERR_CUDA;
   j.out[0] = out;
   j.M = M;
   j.N = N;
