@@ -25,7 +25,7 @@
 #include <cuda_bf16.h>
 #include <type_traits>
 
-#include "tcq_device.cuh"
+#include "tcq_launch.cuh"
 
 namespace tcq {
 
@@ -118,6 +118,8 @@ template <typename T, int N, int TPR, int KEEP>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
                                                             int8_t *__restrict__ q, float *__restrict__ scale) {
   __shared__ uint32_t part[8];
+  after_previous();
+  let_next_start();
   const int t = threadIdx.x % TPR;
   const int64_t r = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
   if (TPR == 32 && r >= rows) return;                   // whole warps: no block barrier follows
@@ -190,6 +192,8 @@ __device__ __forceinline__ uint4 decode16(uint32_t hi, uint32_t lo) {
 template <int L, int LAYOUT>
 __global__ void __launch_bounds__(128) decode_int8_tiles_kernel(const uint32_t *__restrict__ bits, int64_t n_seq,
                                                                 int tiles_c, int wps, int8_t *__restrict__ out) {
+  after_previous();
+  let_next_start();
   const int64_t seq = (int64_t)blockIdx.x * 128 + threadIdx.x;
   if (seq >= n_seq) return;
   const uint32_t *src = bits + seq * wps;
@@ -217,6 +221,8 @@ template <int L>
 __global__ void __launch_bounds__(256) decode_int8_seq_kernel(const uint32_t *__restrict__ bits, int64_t n_items,
                                                               int per_seq, int T, int layout, int wps,
                                                               int8_t *__restrict__ out) {
+  after_previous();
+  let_next_start();
   for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < n_items; g += (int64_t)gridDim.x * 256) {
     const int64_t seq = g / per_seq;
     const int i = (int)(g - seq * per_seq);
@@ -246,8 +252,7 @@ static bool size_ok(int64_t n) { return n < (1ll << 30); }
 template <typename T, int N, int TPR, int KEEP>
 static tcq_status_t quantize_launch(const T *x, int64_t rows, int64_t cols, int8_t *q, float *scale, cudaStream_t s) {
   const unsigned blocks = (unsigned)((rows + 256 / TPR - 1) / (256 / TPR));
-  quantize_rows_kernel<T, N, TPR, KEEP><<<blocks, 256, 0, s>>>(x, rows, cols, q, scale);
-  return launch_status();
+  return launch(quantize_rows_kernel<T, N, TPR, KEEP>, dim3(blocks), 256, 0, 0, s, x, rows, cols, q, scale);
 }
 
 // Whole 16-byte loads where every row starts on such a boundary; a warp a row
@@ -284,17 +289,15 @@ static tcq_status_t decode_launch(const tcq_trellis_t *tr, const uint32_t *bits,
                                   int64_t cols, int8_t *out, int wps, cudaStream_t s) {
   if (cols) {
     const unsigned blocks = (unsigned)((n_seq + 127) / 128);
-    if (layout == TCQ_TAILBITING)
-      decode_int8_tiles_kernel<L, TCQ_TAILBITING><<<blocks, 128, 0, s>>>(bits, n_seq, (int)(cols / 16), wps, out);
-    else
-      decode_int8_tiles_kernel<L, TCQ_FREE_START><<<blocks, 128, 0, s>>>(bits, n_seq, (int)(cols / 16), wps, out);
-  } else {
-    const int per_seq = (tr->seq_len + 15) / 16;
-    const int64_t n = n_seq * per_seq;
-    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 30);
-    decode_int8_seq_kernel<L><<<blocks, 256, 0, s>>>(bits, n, per_seq, tr->seq_len, layout, wps, out);
+    return launch(layout == TCQ_TAILBITING ? decode_int8_tiles_kernel<L, TCQ_TAILBITING>
+                                           : decode_int8_tiles_kernel<L, TCQ_FREE_START>,
+                  dim3(blocks), 128, 0, 0, s, bits, n_seq, (int)(cols / 16), wps, out);
   }
-  return launch_status();
+  const int per_seq = (tr->seq_len + 15) / 16;
+  const int64_t n = n_seq * per_seq;
+  const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 30);
+  return launch(decode_int8_seq_kernel<L>, dim3(blocks), 256, 0, 0, s, bits, n, per_seq, (int)tr->seq_len, layout, wps,
+                out);
 }
 
 extern "C" tcq_status_t tcq_decode_int8(const tcq_trellis_t *tr, const uint32_t *bits, int64_t n_seq, int layout,

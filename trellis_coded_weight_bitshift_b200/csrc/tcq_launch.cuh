@@ -1,0 +1,46 @@
+// Launches that overlap their start with the end of the work before them.
+//
+// A kernel launched with `launch` may become resident while the stream's
+// previous kernel still runs (programmatic dependent launch): it sets up its
+// barriers and tensor memory, then waits in after_previous() until that kernel
+// is complete and its writes are visible, and only then touches global memory.
+// let_next_start() allows the following kernel the same; it is called once every
+// block is past its start.  A kernel before it that never calls it simply
+// completes first.  Measured on 8-bit products of one token (8192 x 8192):
+// 15.5 us a pass without, 13.6 with.
+#pragma once
+
+#include <utility>
+
+#include "tcq_device.cuh"
+
+namespace tcq {
+
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace tcq
+
+namespace tcq_host {
+
+// cluster: blocks of a cluster along x (0: the kernel's own attribute, or none)
+template <typename... P, typename... A>
+inline tcq_status_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                           cudaStream_t stream, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...) == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA;
+}
+
+}  // namespace tcq_host

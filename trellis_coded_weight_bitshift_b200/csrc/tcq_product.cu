@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 
 #include "tcq_activation.cuh"
+#include "tcq_launch.cuh"
 #include "tcq_tensor.cuh"
 
 namespace tcq {
@@ -193,6 +194,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  after_previous();
+  let_next_start();
 
   if (warp == 0 && lane == 0) {
     // ---- loads: this block's rows of A and half of B, counted by the first block's barrier
@@ -393,6 +396,19 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(&tmem_slot, Sh::kTmem);
+  after_previous();
+  const auto load = [&](int kb, int s) {
+    const uint32_t at = ring + s * Sh::kStage, bar = full + 8 * s;
+    const int k = kb * (I8 ? 128 : 64);
+    mbar_expect(bar, Sh::kStage);
+    tma_load(at, &p.w[0], k, (int)n0, bar);
+    if (DUAL) tma_load(at + 16384, &p.w[1], k, (int)n0, bar);
+    tma_load(at + Sh::kWeightBytes, &p.x, k, (int)m0, bar);
+  };
+  const int ahead = min(Sh::kDepth, kb1 - kb0);          // the ring's first round needs no wait
+  if (threadIdx.x == 0)
+    for (int i = 0; i < ahead; ++i) load(kb0 + i, i);
+  let_next_start();
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
@@ -400,16 +416,11 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
 
   if (warp == 0 && lane == 0) {
     int s = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 1;
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
+    for (int kb = kb0 + ahead; kb < kb1; ++kb) {
       if (!mbar_wait(empty + 8 * s, ph ^ 1, &stop)) { ok = false; break; }
-      const uint32_t at = ring + s * Sh::kStage, bar = full + 8 * s;
-      const int k = kb * (I8 ? 128 : 64);
-      mbar_expect(bar, Sh::kStage);
-      tma_load(at, &p.w[0], k, (int)n0, bar);
-      if (DUAL) tma_load(at + 16384, &p.w[1], k, (int)n0, bar);
-      tma_load(at + Sh::kWeightBytes, &p.x, k, (int)m0, bar);
+      load(kb, s);
       if (++s == Sh::kDepth) { s = 0; ph ^= 1; }
     }
     if (!ok)                                             // gave up: the copies in flight land first
@@ -528,6 +539,8 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
 // end is read by bytes, so nothing past it is touched.
 __global__ void __launch_bounds__(256) pitch_rows_kernel(const uint8_t *__restrict__ src, int64_t rows, int64_t bytes,
                                                          int64_t pitch, uint4 *__restrict__ dst) {
+  after_previous();
+  let_next_start();
   const int64_t per = pitch >> 4, n = rows * per, total = rows * bytes;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per, c = (i - r * per) << 4;
@@ -571,6 +584,8 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const T *__restrict__ gr
                                                         const float *__restrict__ up, int64_t rows, int64_t cols,
                                                         int64_t pitch, int act, T *__restrict__ dg,
                                                         T *__restrict__ du) {
+  after_previous();
+  let_next_start();
   const int64_t n = rows * cols;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / cols, c = i - r * cols;
@@ -639,10 +654,9 @@ tcq_status_t ready(Operand &o, const void *p, int64_t rows, int64_t cols, int es
   o = {p, rows, cols, round_up(cols * es, 16), es};
   if (!needs_pitch(rows, cols * es)) return TCQ_OK;
   uint4 *copy = (uint4 *)ws.take(pitch_bytes(rows, cols * es));
-  pitch_rows_kernel<<<blocks_for(rows * (o.pitch / 16)), 256, 0, s>>>((const uint8_t *)p, rows, cols * es, o.pitch,
-                                                                      copy);
   o.p = copy;
-  return launch_status();
+  return launch(pitch_rows_kernel, dim3(blocks_for(rows * (o.pitch / 16))), 256, 0, 0, s, (const uint8_t *)p, rows,
+                cols * es, o.pitch, copy);
 }
 
 bool map_of(CUtensorMap *m, const Operand &o, int box_rows) {
@@ -666,8 +680,7 @@ tcq_status_t launch_pair(PairParams &p, cudaStream_t s) {
   }
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(clusters, most);
   if (p.shares == 1) p.share[0].n = (int)(grid / 2);
-  pair_kernel<I8, DUAL><<<grid, kPairThreads, kPairSmem, s>>>(p);
-  return launch_status();
+  return launch(pair_kernel<I8, DUAL>, dim3(grid), kPairThreads, kPairSmem, 0, s, p);
 }
 
 template <bool I8, bool DUAL, int NT>
@@ -680,18 +693,7 @@ tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
   const int64_t nt = tiles(p.N, 128), mt = tiles(p.M, NT), slots = (int64_t)sm_count() * Sh::kBlocksPerSm;
   int split = 1;
   while (split < 8 && 2 * split * nt * mt <= slots && p.kb >= 8 * split) split *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(nt * split), (unsigned)mt);
-  cfg.blockDim = dim3(192);
-  cfg.dynamicSmemBytes = Sh::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rows_kernel<I8, DUAL, NT>, p) == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA;
+  return launch(rows_kernel<I8, DUAL, NT>, dim3((unsigned)(nt * split), (unsigned)mt), 192, Sh::kSmem, split, s, p);
 }
 
 }  // namespace
@@ -846,12 +848,11 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
   for (Operand &o : d) o = {w.take((size_t)n_tok * pitch), n_tok, n_out, pitch, 2};
   const unsigned blocks = blocks_for(n_tok * n_out);
   if (dtype == TCQ_F16)
-    gate_grad_kernel<<<blocks, 256, 0, s>>>((const __half *)grad_h, gate, up, n_tok, n_out, pitch / 2, act,
-                                            (__half *)d[0].p, (__half *)d[1].p);
+    st = launch(gate_grad_kernel<__half>, dim3(blocks), 256, 0, 0, s, (const __half *)grad_h, gate, up, n_tok, n_out,
+                pitch / 2, act, (__half *)d[0].p, (__half *)d[1].p);
   else
-    gate_grad_kernel<<<blocks, 256, 0, s>>>((const __nv_bfloat16 *)grad_h, gate, up, n_tok, n_out, pitch / 2, act,
-                                            (__nv_bfloat16 *)d[0].p, (__nv_bfloat16 *)d[1].p);
-  st = launch_status();
+    st = launch(gate_grad_kernel<__nv_bfloat16>, dim3(blocks), 256, 0, 0, s, (const __nv_bfloat16 *)grad_h, gate, up,
+                n_tok, n_out, pitch / 2, act, (__nv_bfloat16 *)d[0].p, (__nv_bfloat16 *)d[1].p);
   if (st != TCQ_OK) return st;
 
   PairParams p;
