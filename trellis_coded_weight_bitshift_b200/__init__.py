@@ -61,16 +61,17 @@ def _require_cuda(*tensors: "torch.Tensor | None") -> None:
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device() if t.is_cuda else -1
+        if at < 0:
             raise ValueError("tensors must be CUDA tensors (no CPU fallback)")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors must all be on one device ({dev} and {t.device})")
-    if dev is not None and dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev} but the current device is "
+            dev = at
+        elif at != dev:
+            raise ValueError(f"tensors must all be on one device (cuda:{dev} and cuda:{at})")
+    if dev is not None and dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev} but the current device is "
                          f"cuda:{torch.cuda.current_device()} (select it with torch.cuda.device)")
 
 
@@ -366,8 +367,8 @@ def quantize_int8(x: torch.Tensor):
     if x.dim() != 2 or x.dtype not in _DTYPE:
         raise ValueError("x must be a 2-D float16, bfloat16 or float32 tensor")
     rows, cols = x.shape
-    q = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
-    scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    q = torch.empty(rows, cols, dtype=torch.int8, device=x.device)
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
     check(lib().tcq_quantize_int8(_ptr(x), _DTYPE[x.dtype], rows, cols, _ptr(q), _ptr(scale),
                                   _stream()), "tcq_quantize_int8")
     return q, scale
@@ -390,7 +391,7 @@ def decode_int8(bits: torch.Tensor, L: int, seq_len: int = 256, layout: int = TA
         raise ValueError(f"bits must have {words} words per sequence for this trellis and layout")
     shape = (rows, cols) if out_layout == OUT_TILE16 else (n, seq_len)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int8, device=bits.device)
+        out = torch.empty(*shape, dtype=torch.int8, device=bits.device)
     else:
         _out(out, shape, torch.int8, bits)
     check(lib().tcq_decode_int8(ctypes.byref(tr), _ptr(bits), n, int(layout), int(out_layout),
@@ -400,12 +401,12 @@ def decode_int8(bits: torch.Tensor, L: int, seq_len: int = 256, layout: int = TA
 
 def _int8_operands(a, a_scale, weights, bias=None):
     """Shapes and types of an int8 product's operands; returns (n_tok, n_out, n_in)."""
-    _require_cuda(a, a_scale, *(t for pair in weights for t in pair), bias)
+    _require_cuda(a, a_scale, bias, *weights)
     if a.dim() != 2 or a.dtype != torch.int8:
         raise ValueError("a must be a 2-D int8 tensor [n_tok, n_in]")
     n_tok, n_in = a.shape
-    n_out = weights[0][0].shape[0]
-    for w, ws in weights:
+    n_out = weights[0].shape[0]
+    for w, ws in zip(weights[::2], weights[1::2]):
         if w.dtype != torch.int8 or w.shape != (n_out, n_in):
             raise ValueError(f"weights must be int8 tensors of one shape [n_out, {n_in}]")
         if ws.dtype != torch.float32 or ws.shape != (n_out,):
@@ -420,7 +421,7 @@ def _int8_operands(a, a_scale, weights, bias=None):
 def _result(out, shape, dtype, like):
     if dtype not in _DTYPE:
         raise ValueError("the output type must be float16, bfloat16 or float32")
-    return (torch.empty(shape, dtype=dtype, device=like.device) if out is None
+    return (torch.empty(*shape, dtype=dtype, device=like.device) if out is None
             else _out(out, shape, dtype, like))
 
 
@@ -430,7 +431,7 @@ def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     """out[m, n] = a_scale[m] w_scale[n] (a w^T)[m, n] + bias[n] for int8
     tokens ``a`` [n_tok, n_in] and weights ``w`` [n_out, n_in] with fp32
     scales; the product is exact in 32-bit integers."""
-    n_tok, n_out, n_in = _int8_operands(a, a_scale, ((w, w_scale),), bias)
+    n_tok, n_out, n_in = _int8_operands(a, a_scale, (w, w_scale), bias)
     out = _result(out, (n_tok, n_out), out_dtype, a)
     need = int(lib().tcq_int8_matmul_workspace_size(n_tok, n_out, n_in))
     ws = _use_workspace(workspace, need, a) if need else None
@@ -447,7 +448,7 @@ def int8_gated_ffn(a: torch.Tensor, a_scale: torch.Tensor, w_gate: torch.Tensor,
                    workspace: torch.Tensor | None = None) -> torch.Tensor:
     """The gated feed-forward block on int8 operands: act(g) * u with g and u
     the scaled int8 products of ``a`` with ``w_gate`` and ``w_up``."""
-    n_tok, n_out, n_in = _int8_operands(a, a_scale, ((w_gate, w_gate_scale), (w_up, w_up_scale)))
+    n_tok, n_out, n_in = _int8_operands(a, a_scale, (w_gate, w_gate_scale, w_up, w_up_scale))
     out = _result(out, (n_tok, n_out), out_dtype, a)
     need = int(lib().tcq_int8_gated_ffn_workspace_size(n_tok, n_out, n_in))
     ws = _use_workspace(workspace, need, a) if need else None
@@ -481,7 +482,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: in
     out = _result(out, (n_tok, n_out), x.dtype, x)
     gate = up = None
     if save:
-        gate, up = (torch.empty((n_tok, n_out), dtype=torch.float32, device=x.device) for _ in range(2))
+        gate, up = (torch.empty(n_tok, n_out, dtype=torch.float32, device=x.device) for _ in range(2))
     need = int(lib().tcq_gated_ffn_workspace_size(n_tok, n_out, n_in))
     ws = _use_workspace(workspace, need, x) if need else None
     check(lib().tcq_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _DTYPE[x.dtype], n_tok, n_out, n_in,

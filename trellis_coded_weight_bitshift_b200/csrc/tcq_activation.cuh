@@ -32,11 +32,28 @@ __device__ __forceinline__ void activation_slope(float v, int act, float &a, flo
   }
 }
 
-__device__ __forceinline__ float activation(float v, int act) {
-  if (act == TCQ_ACT_SILU) return v * logistic(v);
-  if (act == TCQ_ACT_GELU) return 0.5f * v * erfcf(-0.70710678f * v);
-  if (act == TCQ_ACT_GELU_TANH) return v * logistic(1.59576912f * v * (1.0f + 0.044715f * v * v));
+template <int ACT>
+__device__ __forceinline__ float activation(float v) {
+  if (ACT == TCQ_ACT_SILU) return v * logistic(v);
+  if (ACT == TCQ_ACT_GELU) return 0.5f * v * erfcf(-0.70710678f * v);
+  if (ACT == TCQ_ACT_GELU_TANH) return v * logistic(1.59576912f * v * (1.0f + 0.044715f * v * v));
   return v < 0.0f ? 0.0f : v;
+}
+
+// g = act(g) * u, N values.  One branch for all of them: a branch for each value
+// made the epilogue the slower half of the kernel (8-bit block 2048 x 2048 x 8192
+// with the tanh form: 74.5 us a pass, 60.5 so).
+template <int ACT, int N>
+__device__ __forceinline__ void gate_as(float (&g)[N], const float (&u)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) g[i] = activation<ACT>(g[i]) * u[i];
+}
+template <int N>
+__device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int act) {
+  if (act == TCQ_ACT_SILU) gate_as<TCQ_ACT_SILU>(g, u);
+  else if (act == TCQ_ACT_GELU) gate_as<TCQ_ACT_GELU>(g, u);
+  else if (act == TCQ_ACT_GELU_TANH) gate_as<TCQ_ACT_GELU_TANH>(g, u);
+  else gate_as<TCQ_ACT_RELU>(g, u);
 }
 
 }  // namespace tcq

@@ -91,7 +91,7 @@ __device__ __forceinline__ void quantize_store(const Values<T, N> &v, float up, 
     return;
   }
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
+  for (int i = 0; 2 * i < N; ++i) {
     const f2_t xx = f2(x[2 * i], x[(2 * i + 1) % N]);
     const f2_t uu = f2fma(xx, f2(inv, inv), f2(kRound, kRound));
     const f2_t rr = f2fma(f2sub(f2(kRound, kRound), uu), f2(scale, scale), xx);

@@ -29,19 +29,21 @@ constexpr int kPairSmem = kStages * kStageBytes + 1024;
 // One product: sums over `segs` pairs of operands a[s], b[s] in turn, or (z > 1)
 // z products with operands a[z] and the same b[0].
 struct Job {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[2], b[2], b_half[2];   // b_half: 64-row boxes, for narrow tiles of a K-major b
   void *out[2];
   int64_t M, N;        // results of one product
   int mt, nt;          // tiles of it
+  int band;            // row tiles of a band
   int kb, segs;        // steps of one segment
   int z;
   int a_mn, b_mn;      // operand stored with its rows along the contraction
   int wide;            // bytes of a store: 32, 16 or one element
 };
 
-// Tiles [lo, hi) of a job, dealt in turn to clusters first .. first + n - 1.
+// Tiles [lo, hi) of a job, dealt in turn to clusters first .. first + n - 1.  A
+// narrow share deals half tiles (256 x 128): lo and hi count those.
 struct Share {
-  int job, first, n;
+  int job, first, n, narrow;
   int64_t lo, hi;
 };
 
@@ -54,7 +56,7 @@ struct Epilogue {
 
 struct PairParams {
   Job job[2];
-  Share share[3];
+  Share share[5];
   int shares;
   int bf16;
   Epilogue e;
@@ -77,14 +79,15 @@ struct Tiles {
     }
     return false;
   }
-  // Bands of eight row tiles, rows first, so that clusters at work share operands in L2.
-  __device__ __forceinline__ void place(const Job &j, int &z, int &m, int &n) const {
-    const int64_t per = (int64_t)j.mt * j.nt;
-    z = j.z > 1 ? (int)(t / per) : 0;
-    const int64_t r = t - z * per, band = r / (8 * (int64_t)j.nt), in = r - band * 8 * j.nt;
-    const int rows = min(8, j.mt - (int)band * 8);
-    m = (int)band * 8 + (int)(in % rows);
-    n = (int)(in / rows);
+  // Row tile m; n counts half tiles of columns.  Tiles go by bands of rows, rows
+  // first, so that clusters at work share operands in L2.
+  __device__ __forceinline__ void place(const Job &j, int narrow, int &z, int &m, int &n) const {
+    const int64_t per = (int64_t)j.mt * j.nt, full = narrow ? t >> 1 : t;
+    z = j.z > 1 ? (int)(full / per) : 0;
+    const int64_t r = full - z * per, band = r / ((int64_t)j.band * j.nt), in = r - band * j.band * j.nt;
+    const int rows = min(j.band, j.mt - (int)band * j.band);
+    m = (int)band * j.band + (int)(in % rows);
+    n = 2 * (int)(in / rows) + (narrow ? (int)(t & 1) : 0);
   }
 };
 
@@ -124,8 +127,13 @@ __device__ __forceinline__ void store16(void *out, int64_t at, int dtype, const 
         store_words((char *)out + 4 * at + 32 * h, w, wide);
       }
     } else {
+      if (dtype == TCQ_F16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], dtype);
+        for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], TCQ_F16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], TCQ_BF16);
+      }
       store_words((char *)out + 2 * at, w, wide);
     }
     return;
@@ -204,20 +212,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     Tiles it;
     while (ok && it.next(p, cluster)) {
+      const int narrow = p.share[it.s].narrow;
       const Job &j = p.job[p.share[it.s].job];
       int z, m, n;
-      it.place(j, z, m, n);
+      it.place(j, narrow, z, m, n);
       const int row = m * 256 + (int)rank * 128;
-      const int col = DUAL ? n * 128 : n * 256 + (int)rank * 128;
-      const CUtensorMap *bd = DUAL ? &j.b[rank] : nullptr;
+      const int col = DUAL ? n * 64 : n * 128 + (int)rank * (narrow ? 64 : 128);
+      const CUtensorMap *bs = narrow && !j.b_mn ? j.b_half : j.b;
+      const uint32_t bytes = narrow ? 2 * kStageBytes - 16384 : 2 * kStageBytes;
       for (int kb = 0; kb < j.kb * j.segs; ++kb) {
         if (!mbar_wait(empty + 8 * s, ph ^ 1, &stop)) { ok = false; break; }
         const int seg = kb >= j.kb ? 1 : 0;
         const int k = (kb - seg * j.kb) * (I8 ? 128 : 64);
         const uint32_t bar = map_to_rank(full + 8 * s, 0);
         const uint32_t a = ring + s * kStageBytes, b = a + 16384;
-        if (rank == 0) mbar_expect(full + 8 * s, 2 * kStageBytes);
-        const CUtensorMap *am = &j.a[seg + z], *bm = DUAL ? bd : &j.b[seg];
+        if (rank == 0) mbar_expect(full + 8 * s, bytes);
+        const CUtensorMap *am = &j.a[seg + z], *bm = bs + (DUAL ? rank : seg);
         if (!j.a_mn) {
           tma_load_pair(a, am, k, row, bar);
         } else {
@@ -228,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tma_load_pair(b, bm, k, col, bar);
         } else {
           tma_load_pair(b, bm, col, k, bar);
-          tma_load_pair(b + 8192, bm, col + 64, k, bar);
+          if (!narrow) tma_load_pair(b + 8192, bm, col + 64, k, bar);
         }
         if (++s == kStages) { s = 0; ph ^= 1; }
       }
@@ -260,7 +270,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!mbar_wait(acc_empty + 8 * buf, ((n_acc >> 1) & 1) ^ 1, &stop)) break;
       tmem_fence_after_sync();
       const uint32_t d = tmem + buf * 256;
-      const uint32_t instr = I8 ? instr_i8(256, 256) : instr_f16(256, 256, p.bf16, j.a_mn, j.b_mn);
+      const int w = p.share[it.s].narrow ? 128 : 256;
+      const uint32_t instr = I8 ? instr_i8(256, w) : instr_f16(256, w, p.bf16, j.a_mn, j.b_mn);
       const uint32_t a_step = j.a_mn ? 2048 >> 4 : 32 >> 4, b_step = j.b_mn ? 2048 >> 4 : 32 >> 4;
       for (int kb = 0; kb < j.kb * j.segs; ++kb) {
         if (!mbar_wait(full + 8 * s, ph, &stop)) { ok = false; break; }
@@ -285,34 +296,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int n_acc = 0;
     Tiles it;
     while (it.next(p, cluster)) {
+      const int narrow = p.share[it.s].narrow;
       const Job &j = p.job[p.share[it.s].job];
       int z, m, n;
-      it.place(j, z, m, n);
+      it.place(j, narrow, z, m, n);
       const int buf = n_acc & 1;
-      const bool got = mbar_wait(acc_full + 8 * buf, (n_acc >> 1) & 1, &stop);
-      if (!__all_sync(0xFFFFFFFFu, got)) break;
-      tmem_fence_after_sync();
       const int64_t row = (int64_t)m * 256 + rank * 128 + quarter * 32 + lane;
       const bool in = row < j.M;
+      const int chunks = (DUAL ? 4 : 8) >> narrow, col0 = half * chunks * 16, up0 = narrow ? 64 : 128;
+      const int64_t n0 = (int64_t)n * (DUAL ? 64 : 128) + col0;
       const float sa = I8 && in ? __ldg(p.e.a_scale + row) : 1.0f;
-      const uint32_t t0 = tmem + buf * 256 + ((uint32_t)quarter << 21);
-      constexpr int kChunks = DUAL ? 4 : 8;
-      const int col0 = half * (DUAL ? 64 : 128);
-      const int64_t n0 = (int64_t)n * (DUAL ? 128 : 256) + col0;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8 * buf, (n_acc >> 1) & 1, &stop))) break;
+      tmem_fence_after_sync();
+      const uint32_t t0 = tmem + buf * 256 + ((uint32_t)quarter << 21) + col0;
 #pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        const int64_t ch = n0 + 16 * c;
-        const int valid = (int)min((int64_t)16, j.N - ch);
+      for (int c = 0; c < chunks; ++c) {
         float g[16], u[16];
         __syncwarp();                                    // rows past the end skipped the last stores
-        tmem_ld16(t0 + col0 + 16 * c, g);
-        if (DUAL) tmem_ld16(t0 + 128 + col0 + 16 * c, u);
-        tmem_wait_ld();
-        if (c == kChunks - 1) {                          // the tile's sums are in registers: the buffer is free
+        tmem_ld16(t0 + 16 * c, g);
+        if (DUAL) tmem_ld16(t0 + up0 + 16 * c, u);
+        tmem_wait16(g);
+        if (DUAL) tmem_wait16(u);
+        if (c == chunks - 1) {                           // the tile's sums are in registers: the buffer is free
           tmem_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive_at(acc_empty + 8 * buf, 0);
         }
+        const int64_t ch = n0 + 16 * c;
+        const int valid = (int)min((int64_t)16, j.N - ch);
         if (!in || valid <= 0) continue;
         const int64_t at = row * j.N + ch;
         finish16<I8>(g, p.e.s0, ch, valid, sa);
@@ -322,8 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             store16(p.e.gate, at, TCQ_F32, g, valid, p.e.wide_save);
             store16(p.e.up, at, TCQ_F32, u, valid, p.e.wide_save);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) g[i] = activation(g[i], p.e.act) * u[i];
+          gate(g, u, p.e.act);
         } else if (I8 && p.e.bias) {
           float b[16];
           channel16(p.e.bias, ch, valid, b);
@@ -452,8 +462,7 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
   } else if (warp >= 2) {
     // sums to shared memory, [column][channel]: the ring is free once all products are done
     const int quarter = warp & 3;
-    const bool got = mbar_wait(acc_full, 0, &stop);
-    if (__all_sync(0xFFFFFFFFu, got)) {
+    if (__all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, &stop))) {
       tmem_fence_after_sync();
       const int cols = (int)min((int64_t)NT, p.M - m0);
       const uint32_t ch = ring + 4 * (quarter * 32 + lane);
@@ -512,9 +521,9 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
           p.e.gate[at + k] = gv[k];
           p.e.up[at + k] = uv[k];
         }
-        gv[k] = activation(gv[k], p.e.act) * uv[k];
       }
     }
+    if (DUAL) gate(gv, uv, p.e.act);
     if (valid == 4 && p.wide4) {
       if (p.e.dtype == TCQ_F32)
         *reinterpret_cast<float4 *>((float *)p.out + at) = make_float4(gv[0], gv[1], gv[2], gv[3]);
@@ -578,22 +587,46 @@ template <typename T> __device__ __forceinline__ T narrow(float v);
 template <> __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// dg = grad u act'(g), du = grad act(g), in rows `pitch` elements apart.
-template <typename T>
+// dg = grad u act'(g), du = grad act(g), in rows `pitch` elements apart; eight
+// values a thread where rows start on 16-byte boundaries (N = 8), else one.
+template <typename T, int N>
 __global__ void __launch_bounds__(256) gate_grad_kernel(const T *__restrict__ grad, const float *__restrict__ gate,
                                                         const float *__restrict__ up, int64_t rows, int64_t cols,
                                                         int64_t pitch, int act, T *__restrict__ dg,
                                                         T *__restrict__ du) {
   after_previous();
   let_next_start();
-  const int64_t n = rows * cols;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / cols, c = i - r * cols;
-    float a, d;
-    activation_slope(gate[i], act, a, d);
-    const float h = widen<T>(grad[i]);
-    dg[r * pitch + c] = narrow<T>(h * up[i] * d);
-    du[r * pitch + c] = narrow<T>(h * a);
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * N;
+  if (c >= cols) return;
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int64_t at = r * cols + c, to = r * pitch + c;
+    if (N == 1) {
+      float a, d;
+      activation_slope(__ldg(gate + at), act, a, d);
+      const float h = widen<T>(grad[at]);
+      dg[to] = narrow<T>(h * __ldg(up + at) * d);
+      du[to] = narrow<T>(h * a);
+    } else {
+      const uint4 hv = __ldg(reinterpret_cast<const uint4 *>(grad + at));
+      const float4 g0 = __ldg(reinterpret_cast<const float4 *>(gate + at)),
+                   g1 = __ldg(reinterpret_cast<const float4 *>(gate + at) + 1),
+                   u0 = __ldg(reinterpret_cast<const float4 *>(up + at)),
+                   u1 = __ldg(reinterpret_cast<const float4 *>(up + at) + 1);
+      const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+      const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+      const T *h = reinterpret_cast<const T *>(&hv);
+      __align__(16) T og[8], ou[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float a, d;
+        activation_slope(g[i], act, a, d);
+        const float v = widen<T>(h[i]);
+        og[i] = narrow<T>(v * u[i] * d);
+        ou[i] = narrow<T>(v * a);
+      }
+      *reinterpret_cast<uint4 *>(dg + to) = *reinterpret_cast<const uint4 *>(og);
+      *reinterpret_cast<uint4 *>(du + to) = *reinterpret_cast<const uint4 *>(ou);
+    }
   }
 }
 
@@ -663,24 +696,63 @@ bool map_of(CUtensorMap *m, const Operand &o, int box_rows) {
   return make_map(m, o.p, o.es, o.rows, o.cols, o.pitch, box_rows);
 }
 
+// Row tiles of a band: the second operand is read from memory once for each
+// band, so bands are as tall as leaves the first operand's rows (32 KB a step and
+// tile) within 24 MB of the 126 MB L2, at least 8, and of equal height.
+int band_of(const Job &j) {
+  const int64_t most = std::max<int64_t>(8, (24 << 20) / (32768ll * j.kb * j.segs));
+  return (int)tiles(j.mt, tiles(j.mt, most));
+}
+
+// The tiles of one or two jobs, dealt to the clusters.  The job with the longer
+// tiles goes first; clusters that its last round leaves idle take as many of the
+// other's tiles as that round lasts; then the rest goes round.  What is left of
+// the last round, if it occupies at most half of the clusters, is dealt in half
+// tiles.  Measured: gradients of 4096 x 2048 x 8192 447 us for all three in one
+// launch (elementwise pass counted), grad_x alone 300, the weights' two alone 288;
+// gated block 3001 x 2048 x 8192 (768 tiles, 74 clusters) 169.6 us in whole tiles,
+// 168.9 with the last 28 halved (power, not the idle SMs, sets the time there).
+void deal(PairParams &p, int jobs, int clusters) {
+  p.shares = 0;
+  for (int i = 0; i < jobs; ++i) p.job[i].band = band_of(p.job[i]);
+  const auto give = [&](int job, int64_t first, int64_t n, int narrow, int64_t lo, int64_t hi) {
+    if (hi > lo) p.share[p.shares++] = {job, (int)first, (int)n, narrow, lo, hi};
+  };
+  const auto count = [&](int j) { return (int64_t)p.job[j].mt * p.job[j].nt * p.job[j].z; };
+  const auto finish = [&](int j, int64_t lo) {
+    const int64_t hi = count(j), rest = (hi - lo) % clusters;
+    const bool halve = rest > 0 && 2 * rest <= clusters;
+    give(j, 0, clusters, 0, lo, halve ? hi - rest : hi);
+    if (halve) give(j, 0, clusters, 1, 2 * (hi - rest), 2 * hi);
+  };
+  if (jobs == 1) return finish(0, 0);
+  int64_t cost[2];
+  for (int j = 0; j < 2; ++j) cost[j] = (int64_t)p.job[j].kb * p.job[j].segs;
+  const int big = cost[0] >= cost[1] ? 0 : 1, small = 1 - big;
+  int64_t t = count(big), c = cost[big];
+  const bool halve = 2 * t <= clusters;
+  if (halve) {
+    t *= 2;
+    c = (c + 1) / 2;
+  }
+  give(big, 0, clusters, halve, 0, t);
+  const int64_t used = t % clusters, idle = used ? clusters - used : 0;
+  const int64_t fill = std::min(count(small), idle * ((c + cost[small] / 2) / cost[small]));
+  give(small, used, idle, 0, 0, fill);
+  if (fill < count(small)) finish(small, fill);
+}
+
 template <bool I8, bool DUAL>
-tcq_status_t launch_pair(PairParams &p, cudaStream_t s) {
+tcq_status_t launch_pair(PairParams &p, int jobs, cudaStream_t s) {
   if (cudaFuncSetAttribute(pair_kernel<I8, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) !=
       cudaSuccess)
     return TCQ_ERR_CUDA;
   const int clusters = std::max(1, sm_count() / 2);
-  int64_t most = 0;
-  if (p.shares == 0) {                                   // one job, dealt over all clusters
-    const int64_t n = (int64_t)p.job[0].mt * p.job[0].nt * p.job[0].z;
-    p.share[0] = {0, 0, clusters, 0, n};
-    p.shares = 1;
-    most = n;
-  } else {
-    most = clusters;
-  }
-  const unsigned grid = 2 * (unsigned)std::min<int64_t>(clusters, most);
-  if (p.shares == 1) p.share[0].n = (int)(grid / 2);
-  return launch(pair_kernel<I8, DUAL>, dim3(grid), kPairThreads, kPairSmem, 0, s, p);
+  deal(p, jobs, clusters);
+  int64_t grid = 0;                                      // clusters that get a tile
+  for (int i = 0; i < p.shares; ++i)
+    grid = std::max<int64_t>(grid, p.share[i].first + std::min<int64_t>(p.share[i].n, p.share[i].hi - p.share[i].lo));
+  return launch(pair_kernel<I8, DUAL>, dim3(2 * (unsigned)grid), kPairThreads, kPairSmem, 0, s, p);
 }
 
 template <bool I8, bool DUAL, int NT>
@@ -756,13 +828,12 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
                       : launch_rows<I8, DUAL, 128>(r, s);
   }
   PairParams p;
-  p.shares = 0;
   p.bf16 = bf16;
   p.e = e;
   Job &j = p.job[0];
   if (!map_of(&j.a[0], A, 128)) return TCQ_ERR_CUDA;
   for (int i = 0; i < (DUAL ? 2 : 1); ++i)
-    if (!map_of(&j.b[i], B[i], 128)) return TCQ_ERR_CUDA;
+    if (!map_of(&j.b[i], B[i], 128) || !map_of(&j.b_half[i], B[i], 64)) return TCQ_ERR_CUDA;
   j.out[0] = out;
   j.M = M;
   j.N = N;
@@ -773,7 +844,7 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
   j.z = 1;
   j.a_mn = j.b_mn = 0;
   j.wide = width(out, N, type_size(e.dtype));
-  return launch_pair<I8, DUAL>(p, s);
+  return launch_pair<I8, DUAL>(p, 1, s);
 }
 
 extern "C" tcq_status_t tcq_int8_matmul(const int8_t *a, const float *a_scale, const int8_t *w, const float *w_scale,
@@ -823,6 +894,15 @@ extern "C" tcq_status_t tcq_gated_ffn(const void *x, const void *w_gate, const v
                               (cudaStream_t)stream);
 }
 
+template <typename T>
+static tcq_status_t gate_grads(const void *grad, const float *gate, const float *up, int64_t rows, int64_t cols,
+                               int64_t pitch, int act, const void *dg, const void *du, cudaStream_t s) {
+  const bool whole = cols % 8 == 0;
+  const dim3 grid((unsigned)tiles(cols, whole ? 2048 : 256), (unsigned)std::min<int64_t>(rows, 65535));
+  return launch(whole ? gate_grad_kernel<T, 8> : gate_grad_kernel<T, 1>, grid, 256, 0, 0, s, (const T *)grad, gate, up,
+                rows, cols, pitch / 2, act, (T *)dg, (T *)du);
+}
+
 extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, const float *gate,
                                                const float *up, const void *grad_h, int dtype, int64_t n_tok,
                                                int64_t n_out, int64_t n_in, int act, void *grad_x, void *grad_w_gate,
@@ -846,21 +926,17 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
   const int64_t pitch = round_up(2 * n_out, 16);
   Operand d[2], X, W[2];
   for (Operand &o : d) o = {w.take((size_t)n_tok * pitch), n_tok, n_out, pitch, 2};
-  const unsigned blocks = blocks_for(n_tok * n_out);
-  if (dtype == TCQ_F16)
-    st = launch(gate_grad_kernel<__half>, dim3(blocks), 256, 0, 0, s, (const __half *)grad_h, gate, up, n_tok, n_out,
-                pitch / 2, act, (__half *)d[0].p, (__half *)d[1].p);
-  else
-    st = launch(gate_grad_kernel<__nv_bfloat16>, dim3(blocks), 256, 0, 0, s, (const __nv_bfloat16 *)grad_h, gate, up,
-                n_tok, n_out, pitch / 2, act, (__nv_bfloat16 *)d[0].p, (__nv_bfloat16 *)d[1].p);
+  st = dtype == TCQ_F16 ? gate_grads<__half>(grad_h, gate, up, n_tok, n_out, pitch, act, d[0].p, d[1].p, s)
+                        : gate_grads<__nv_bfloat16>(grad_h, gate, up, n_tok, n_out, pitch, act, d[0].p, d[1].p, s);
   if (st != TCQ_OK) return st;
 
   PairParams p;
   p.bf16 = dtype == TCQ_BF16;
   p.e = {dtype, 0, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0};
-  Job &j = p.job[0];
+  int jobs = 0;
   if (grad_x) {
     // one sum over both halves: dg Wg, then du Wu; the weights' rows run along it
+    Job &j = p.job[jobs++];
     for (int i = 0; i < 2; ++i) {
       st = ready(W[i], i ? w_up : w_gate, n_out, n_in, 2, w, s);
       if (st != TCQ_OK) return st;
@@ -868,43 +944,38 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
     }
     j.out[0] = grad_x;
     j.M = n_tok;
-    j.N = n_in;
-    j.mt = (int)tiles(n_tok, 256);
-    j.nt = (int)tiles(n_in, 256);
     j.kb = (int)tiles(n_out, 64);
     j.segs = 2;
     j.z = 1;
     j.a_mn = 0;
-    j.b_mn = 1;
     j.wide = width(grad_x, n_in, 2);
-    p.shares = 0;
-    st = launch_pair<false, false>(p, s);
-    if (st != TCQ_OK) return st;
   }
   if (grad_w_gate || grad_w_up) {
     // dg^T x and du^T x: both operands' rows (tokens) run along the sum
+    Job &j = p.job[jobs++];
     st = ready(X, x, n_tok, n_in, 2, w, s);
     if (st != TCQ_OK) return st;
     if (!map_of(&j.b[0], X, 64)) return TCQ_ERR_CUDA;
-    int z = 0;
+    j.z = 0;
     j.wide = 32;
     for (int i = 0; i < 2; ++i) {
       void *g = i ? grad_w_up : grad_w_gate;
       if (!g) continue;
-      if (!map_of(&j.a[z], d[i], 64)) return TCQ_ERR_CUDA;
-      j.out[z++] = g;
+      if (!map_of(&j.a[j.z], d[i], 64)) return TCQ_ERR_CUDA;
+      j.out[j.z++] = g;
       j.wide = std::min(j.wide, width(g, n_in, 2));
     }
     j.M = n_out;
-    j.N = n_in;
-    j.mt = (int)tiles(n_out, 256);
-    j.nt = (int)tiles(n_in, 256);
     j.kb = (int)tiles(n_tok, 64);
     j.segs = 1;
-    j.z = z;
-    j.a_mn = j.b_mn = 1;
-    p.shares = 0;
-    st = launch_pair<false, false>(p, s);
+    j.a_mn = 1;
   }
-  return st;
+  for (int i = 0; i < jobs; ++i) {
+    Job &j = p.job[i];
+    j.N = n_in;
+    j.b_mn = 1;
+    j.mt = (int)tiles(j.M, 256);
+    j.nt = (int)tiles(n_in, 256);
+  }
+  return launch_pair<false, false>(p, jobs, s);
 }

@@ -37,10 +37,13 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t rank) {
       "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];}" ::"r"(bar), "r"(rank)
       : "memory");
 }
+// One look at the barrier, suspended in hardware for up to a millisecond.  The
+// hint matters: spinning warps take power from the tensor cores (an 8-bit
+// product 3001 x 8192 x 8192 took 162 us with the default look, 151 with this).
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{.reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "{.reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000000;\n"
       "selp.u32 %0, 1, 0, p;}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -90,9 +93,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
-}
 // A tile of one block's operand; `bar` may be the cluster's first block's.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
   asm volatile(
@@ -129,6 +129,16 @@ __host__ __device__ constexpr uint32_t instr_f16(int m, int n, int bf16, int a_m
 }
 __host__ __device__ constexpr uint32_t instr_i8(int m, int n) {
   return 2u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+
+// Waits for this thread's tensor-memory loads and ties the values to the wait,
+// so that nothing that uses them moves before it.
+__device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
 }
 
 template <bool I8, bool PAIR>
