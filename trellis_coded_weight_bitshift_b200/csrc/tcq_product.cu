@@ -406,6 +406,14 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(&tmem_slot, Sh::kTmem);
+  const int ahead = min(Sh::kDepth, kb1 - kb0);          // the ring's first round needs no wait
+  if (threadIdx.x == 64) {
+    // its weights to L2 while the previous kernel ends (should that kernel write them, L2 stays coherent)
+    for (int i = 0; i < ahead; ++i) {
+      tma_prefetch(&p.w[0], (kb0 + i) * (I8 ? 128 : 64), (int)n0);
+      if (DUAL) tma_prefetch(&p.w[1], (kb0 + i) * (I8 ? 128 : 64), (int)n0);
+    }
+  }
   after_previous();
   const auto load = [&](int kb, int s) {
     const uint32_t at = ring + s * Sh::kStage, bar = full + 8 * s;
@@ -415,10 +423,22 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
     if (DUAL) tma_load(at + 16384, &p.w[1], k, (int)n0, bar);
     tma_load(at + Sh::kWeightBytes, &p.x, k, (int)m0, bar);
   };
-  const int ahead = min(Sh::kDepth, kb1 - kb0);          // the ring's first round needs no wait
   if (threadIdx.x == 0)
     for (int i = 0; i < ahead; ++i) load(kb0 + i, i);
-  let_next_start();
+  // the scales of this thread's first results, while the operands stream
+  const int quads = 32 / split, cols = (int)min((int64_t)NT, p.M - m0);
+  float sa0 = 0.0f, s00[4] = {}, s10[4] = {};
+  if (I8 && threadIdx.x < quads * cols) {
+    const int64_t ch = n0 + 4 * (rank * quads + (int)threadIdx.x % quads);
+    sa0 = __ldg(p.e.a_scale + m0 + threadIdx.x / quads);
+    const float *second = DUAL ? p.e.s1 : p.e.bias;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ch + k >= p.N) continue;
+      s00[k] = __ldg(p.e.s0 + ch + k);
+      if (second) s10[k] = __ldg(second + ch + k);
+    }
+  }
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
@@ -433,6 +453,7 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
       load(kb, s);
       if (++s == Sh::kDepth) { s = 0; ph ^= 1; }
     }
+    let_next_start();                                    // its blocks start while these finish
     if (!ok)                                             // gave up: the copies in flight land first
       for (int i = 0; i < Sh::kDepth; ++i) {
         s = s ? s - 1 : Sh::kDepth - 1;
@@ -464,7 +485,6 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
     const int quarter = warp & 3;
     if (__all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, &stop))) {
       tmem_fence_after_sync();
-      const int cols = (int)min((int64_t)NT, p.M - m0);
       const uint32_t ch = ring + 4 * (quarter * 32 + lane);
 #pragma unroll 1
       for (int c = 0; c < Sh::kCols; c += 16) {
@@ -488,7 +508,6 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
   cluster_sync();
 
   // each block finishes 128 / split of the channels, four a thread
-  const int quads = 32 / split, cols = (int)min((int64_t)NT, p.M - m0);
   uint32_t peer[8];
 #pragma unroll
   for (int r = 0; r < 8; ++r) peer[r] = r < split ? map_to_rank(ring, r) : 0;
@@ -511,10 +530,11 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
     for (int k = 0; k < 4; ++k) {
       if (k >= valid) continue;
       if (I8) {
-        const float sa = __ldg(p.e.a_scale + row);
-        gv[k] = (float)__float_as_int(gv[k]) * sa * __ldg(p.e.s0 + ch + k);
-        if (DUAL) uv[k] = (float)__float_as_int(uv[k]) * sa * __ldg(p.e.s1 + ch + k);
-        else if (p.e.bias) gv[k] = __fadd_rn(gv[k], __ldg(p.e.bias + ch + k));
+        const bool first = i < 192;
+        const float sa = first ? sa0 : __ldg(p.e.a_scale + row);
+        gv[k] = (float)__float_as_int(gv[k]) * sa * (first ? s00[k] : __ldg(p.e.s0 + ch + k));
+        if (DUAL) uv[k] = (float)__float_as_int(uv[k]) * sa * (first ? s10[k] : __ldg(p.e.s1 + ch + k));
+        else if (p.e.bias) gv[k] = __fadd_rn(gv[k], first ? s10[k] : __ldg(p.e.bias + ch + k));
       }
       if (DUAL) {
         if (!I8 && p.e.gate) {

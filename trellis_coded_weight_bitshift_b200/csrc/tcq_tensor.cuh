@@ -108,6 +108,10 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *m, int
       "l"(m), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// A tile on its way to L2 only.
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *m, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
