@@ -34,6 +34,10 @@ struct Job {
   int64_t M, N;        // results of one product
   int mt, nt;          // tiles of it
   int band;            // row tiles of a band
+  int split;           // parts of the contraction; with more than one, raw sums go to `part`
+  int planes;          // of `part`, [split][planes][M][pitch]: gate and up, or the z products
+  int64_t pitch;
+  float *part;
   int kb, segs;        // steps of one segment
   int z;
   int a_mn, b_mn;      // operand stored with its rows along the contraction
@@ -44,7 +48,7 @@ struct Job {
 // narrow share deals half tiles (256 x 128): lo and hi count those.
 struct Share {
   int job, first, n, narrow;
-  int64_t lo, hi;
+  uint32_t lo, hi;
 };
 
 struct Epilogue {
@@ -65,7 +69,7 @@ struct PairParams {
 // The tiles of one cluster, in order.
 struct Tiles {
   int s;
-  int64_t t;
+  uint32_t t;
   __device__ __forceinline__ Tiles() : s(-1), t(0) {}
   __device__ __forceinline__ bool next(const PairParams &p, int cluster) {
     if (s >= 0) {
@@ -74,19 +78,40 @@ struct Tiles {
     }
     while (++s < p.shares) {
       const int c = cluster - p.share[s].first;
-      t = p.share[s].lo + c;
+      t = p.share[s].lo + (uint32_t)c;
       if (c >= 0 && c < p.share[s].n && t < p.share[s].hi) return true;
     }
     return false;
   }
-  // Row tile m; n counts half tiles of columns.  Tiles go by bands of rows, rows
-  // first, so that clusters at work share operands in L2.
-  __device__ __forceinline__ void place(const Job &j, int narrow, int &z, int &m, int &n) const {
-    const int64_t per = (int64_t)j.mt * j.nt, full = narrow ? t >> 1 : t;
-    z = j.z > 1 ? (int)(full / per) : 0;
-    const int64_t r = full - z * per, band = r / ((int64_t)j.band * j.nt), in = r - band * j.band * j.nt;
-    const int rows = min(j.band, j.mt - (int)band * j.band);
-    m = (int)band * j.band + (int)(in % rows);
+};
+
+// A tile: product z, row tile m, n half tiles of columns, steps [k0, k1) of the
+// contraction as its part s.
+struct Place {
+  int z, m, n, s, k0, k1;
+  // Tiles go by bands of rows, rows first, so that clusters at work share operands
+  // in L2.  All in 32 bits (the host sees to it): 64-bit divisions took a
+  // microsecond of every launch.
+  __device__ __forceinline__ Place(const Job &j, uint32_t t, int narrow) {
+    const uint32_t steps = (uint32_t)(j.kb * j.segs), split = (uint32_t)j.split;
+    s = 0;
+    k0 = 0;
+    k1 = (int)steps;
+    if (split > 1) {
+      s = (int)(t % split);
+      t /= split;
+      k0 = (int)(steps * (uint32_t)s / split);
+      k1 = (int)(steps * (uint32_t)(s + 1) / split);
+    }
+    uint32_t r = narrow ? t >> 1 : t;
+    z = 0;
+    if (j.z > 1 && r >= (uint32_t)(j.mt * j.nt)) {
+      r -= (uint32_t)(j.mt * j.nt);
+      z = 1;
+    }
+    const uint32_t per = (uint32_t)(j.band * j.nt), band = r / per, in = r - band * per;
+    const uint32_t rows = min((uint32_t)j.band, (uint32_t)j.mt - band * j.band);
+    m = (int)(band * j.band + in % rows);
     n = 2 * (int)(in / rows) + (narrow ? (int)(t & 1) : 0);
   }
 };
@@ -214,20 +239,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     while (ok && it.next(p, cluster)) {
       const int narrow = p.share[it.s].narrow;
       const Job &j = p.job[p.share[it.s].job];
-      int z, m, n;
-      it.place(j, narrow, z, m, n);
-      const int row = m * 256 + (int)rank * 128;
-      const int col = DUAL ? n * 64 : n * 128 + (int)rank * (narrow ? 64 : 128);
+      const Place at(j, it.t, narrow);
+      const int row = at.m * 256 + (int)rank * 128;
+      const int col = DUAL ? at.n * 64 : at.n * 128 + (int)rank * (narrow ? 64 : 128);
       const CUtensorMap *bs = narrow && !j.b_mn ? j.b_half : j.b;
       const uint32_t bytes = narrow ? 2 * kStageBytes - 16384 : 2 * kStageBytes;
-      for (int kb = 0; kb < j.kb * j.segs; ++kb) {
+      for (int kb = at.k0; kb < at.k1; ++kb) {
         if (!mbar_wait(empty + 8 * s, ph ^ 1, &stop)) { ok = false; break; }
         const int seg = kb >= j.kb ? 1 : 0;
         const int k = (kb - seg * j.kb) * (I8 ? 128 : 64);
         const uint32_t bar = map_to_rank(full + 8 * s, 0);
         const uint32_t a = ring + s * kStageBytes, b = a + 16384;
         if (rank == 0) mbar_expect(full + 8 * s, bytes);
-        const CUtensorMap *am = &j.a[seg + z], *bm = bs + (DUAL ? rank : seg);
+        const CUtensorMap *am = &j.a[seg + at.z], *bm = bs + (DUAL ? rank : seg);
         if (!j.a_mn) {
           tma_load_pair(a, am, k, row, bar);
         } else {
@@ -273,14 +297,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int w = p.share[it.s].narrow ? 128 : 256;
       const uint32_t instr = I8 ? instr_i8(256, w) : instr_f16(256, w, p.bf16, j.a_mn, j.b_mn);
       const uint32_t a_step = j.a_mn ? 2048 >> 4 : 32 >> 4, b_step = j.b_mn ? 2048 >> 4 : 32 >> 4;
-      for (int kb = 0; kb < j.kb * j.segs; ++kb) {
+      const Place place(j, it.t, p.share[it.s].narrow);
+      for (int kb = place.k0; kb < place.k1; ++kb) {
         if (!mbar_wait(full + 8 * s, ph, &stop)) { ok = false; break; }
         tmem_fence_after_sync();
         const uint32_t at = ring + s * kStageBytes;
         uint64_t a = operand_desc(at, j.a_mn), b = operand_desc(at + 16384, j.b_mn);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          mma<I8, true>(d, a, b, instr, kb > 0 || i > 0);
+          mma<I8, true>(d, a, b, instr, kb > place.k0 || i > 0);
           a += a_step;
           b += b_step;
         }
@@ -298,13 +323,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     while (it.next(p, cluster)) {
       const int narrow = p.share[it.s].narrow;
       const Job &j = p.job[p.share[it.s].job];
-      int z, m, n;
-      it.place(j, narrow, z, m, n);
+      const Place at(j, it.t, narrow);
       const int buf = n_acc & 1;
-      const int64_t row = (int64_t)m * 256 + rank * 128 + quarter * 32 + lane;
+      const int64_t row = (int64_t)at.m * 256 + rank * 128 + quarter * 32 + lane;
       const bool in = row < j.M;
       const int chunks = (DUAL ? 4 : 8) >> narrow, col0 = half * chunks * 16, up0 = narrow ? 64 : 128;
-      const int64_t n0 = (int64_t)n * (DUAL ? 64 : 128) + col0;
+      const int64_t n0 = (int64_t)at.n * (DUAL ? 64 : 128) + col0;
       const float sa = I8 && in ? __ldg(p.e.a_scale + row) : 1.0f;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8 * buf, (n_acc >> 1) & 1, &stop))) break;
       tmem_fence_after_sync();
@@ -325,13 +349,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int64_t ch = n0 + 16 * c;
         const int valid = (int)min((int64_t)16, j.N - ch);
         if (!in || valid <= 0) continue;
-        const int64_t at = row * j.N + ch;
+        if (j.split > 1) {
+          float *part = j.part + (((int64_t)at.s * j.planes + (DUAL ? 0 : at.z)) * j.M + row) * j.pitch + ch;
+          store16(part, 0, TCQ_F32, g, 16, 32);
+          if (DUAL) store16(part + j.M * j.pitch, 0, TCQ_F32, u, 16, 32);
+          continue;
+        }
+        const int64_t to = row * j.N + ch;
         finish16<I8>(g, p.e.s0, ch, valid, sa);
         if (DUAL) {
           finish16<I8>(u, p.e.s1, ch, valid, sa);
           if (!I8 && p.e.gate) {
-            store16(p.e.gate, at, TCQ_F32, g, valid, p.e.wide_save);
-            store16(p.e.up, at, TCQ_F32, u, valid, p.e.wide_save);
+            store16(p.e.gate, to, TCQ_F32, g, valid, p.e.wide_save);
+            store16(p.e.up, to, TCQ_F32, u, valid, p.e.wide_save);
           }
           gate(g, u, p.e.act);
         } else if (I8 && p.e.bias) {
@@ -340,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) g[i] = __fadd_rn(g[i], b[i]);
         }
-        store16(j.out[z], at, p.e.dtype, g, valid, j.wide);
+        store16(j.out[at.z], to, p.e.dtype, g, valid, j.wide);
       }
       ++n_acc;
     }
@@ -380,6 +410,93 @@ __device__ __forceinline__ void add4(float4 &s, const float4 &v, bool i8) {
     s.w = __int_as_float(__float_as_int(s.w) + __float_as_int(v.w));
   } else {
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+}
+
+// Four neighbouring channels of a token: sums to results.  Scales that were read
+// before come in `sa`, `c0` and `c1` (the up projection's, or the bias).
+template <bool I8, bool DUAL>
+__device__ __forceinline__ void finish4(const Epilogue &e, const float4 &g, const float4 &u, int64_t row, int64_t N,
+                                        int64_t ch, int valid, bool wide, void *out, const float *sa,
+                                        const float (&c0)[4], const float (&c1)[4]) {
+  float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
+  const int64_t at = row * N + ch;
+  if (I8) {
+    const float s = sa ? *sa : __ldg(e.a_scale + row);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= valid) continue;
+      gv[k] = (float)__float_as_int(gv[k]) * s * (sa ? c0[k] : __ldg(e.s0 + ch + k));
+      if (DUAL) uv[k] = (float)__float_as_int(uv[k]) * s * (sa ? c1[k] : __ldg(e.s1 + ch + k));
+      else if (e.bias) gv[k] = __fadd_rn(gv[k], sa ? c1[k] : __ldg(e.bias + ch + k));
+    }
+  }
+  if (DUAL) {
+    if (!I8 && e.gate) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k >= valid) continue;
+        e.gate[at + k] = gv[k];
+        e.up[at + k] = uv[k];
+      }
+    }
+    gate(gv, uv, e.act);
+  }
+  if (valid == 4 && wide) {
+    if (e.dtype == TCQ_F32)
+      *reinterpret_cast<float4 *>((float *)out + at) = make_float4(gv[0], gv[1], gv[2], gv[3]);
+    else
+      *reinterpret_cast<uint2 *>((uint16_t *)out + at) =
+          make_uint2(pack2(gv[0], gv[1], e.dtype), pack2(gv[2], gv[3], e.dtype));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= valid) continue;
+      if (e.dtype == TCQ_F32) ((float *)out)[at + k] = gv[k];
+      else ((uint16_t *)out)[at + k] = (uint16_t)pack2(gv[k], 0.0f, e.dtype);
+    }
+  }
+}
+
+// Adds the parts of a split product in order and finishes them, four channels a
+// thread; blockIdx.z: the product.
+struct Join {
+  const float *part;
+  int split, planes, wide4;
+  int64_t M, N, pitch;
+  void *out[2];
+  Epilogue e;
+};
+
+template <bool I8, bool DUAL>
+__global__ void __launch_bounds__(256) join_kernel(const Join p) {
+  after_previous();
+  let_next_start();
+  const int64_t quads = (p.N + 3) / 4;
+  const int z = blockIdx.z;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.M * quads; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / quads, ch = (i - row * quads) * 4;
+    float4 g = make_float4(0, 0, 0, 0), u = g;
+    const float *at = p.part + ((int64_t)z * p.M + row) * p.pitch + ch;
+    const int64_t plane = p.M * p.pitch, part = plane * p.planes;
+    // four parts' loads at a time: one after the other their latencies would add up
+    for (int s = 0; s < p.split; s += 4) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool there = s + k < p.split;
+        a[k] = there ? __ldg(reinterpret_cast<const float4 *>(at + (s + k) * part)) : make_float4(0, 0, 0, 0);
+        if (DUAL) b[k] = there ? __ldg(reinterpret_cast<const float4 *>(at + (s + k) * part + plane)) : make_float4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        add4(g, a[k], I8);
+        if (DUAL) add4(u, b[k], I8);
+      }
+    }
+    const float none[4] = {};
+    finish4<I8, DUAL>(p.e, g, u, row, p.N, ch, (int)min((int64_t)4, p.N - ch), p.wide4, p.out[z], nullptr, none,
+                      none);
   }
 }
 
@@ -524,40 +641,8 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
       add4(g, ld_cluster4(peer[r] + off), I8);
       if (DUAL) add4(u, ld_cluster4(peer[r] + off + 512 * NT), I8);
     }
-    float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
-    const int64_t at = row * p.N + ch;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k >= valid) continue;
-      if (I8) {
-        const bool first = i < 192;
-        const float sa = first ? sa0 : __ldg(p.e.a_scale + row);
-        gv[k] = (float)__float_as_int(gv[k]) * sa * (first ? s00[k] : __ldg(p.e.s0 + ch + k));
-        if (DUAL) uv[k] = (float)__float_as_int(uv[k]) * sa * (first ? s10[k] : __ldg(p.e.s1 + ch + k));
-        else if (p.e.bias) gv[k] = __fadd_rn(gv[k], first ? s10[k] : __ldg(p.e.bias + ch + k));
-      }
-      if (DUAL) {
-        if (!I8 && p.e.gate) {
-          p.e.gate[at + k] = gv[k];
-          p.e.up[at + k] = uv[k];
-        }
-      }
-    }
-    if (DUAL) gate(gv, uv, p.e.act);
-    if (valid == 4 && p.wide4) {
-      if (p.e.dtype == TCQ_F32)
-        *reinterpret_cast<float4 *>((float *)p.out + at) = make_float4(gv[0], gv[1], gv[2], gv[3]);
-      else
-        *reinterpret_cast<uint2 *>((uint16_t *)p.out + at) =
-            make_uint2(pack2(gv[0], gv[1], p.e.dtype), pack2(gv[2], gv[3], p.e.dtype));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k >= valid) continue;
-        if (p.e.dtype == TCQ_F32) ((float *)p.out)[at + k] = gv[k];
-        else ((uint16_t *)p.out)[at + k] = (uint16_t)pack2(gv[k], 0.0f, p.e.dtype);
-      }
-    }
+    const bool first = i < 192;
+    finish4<I8, DUAL>(p.e, g, u, row, p.N, ch, valid, p.wide4, p.out, first ? &sa0 : nullptr, s00, s10);
   }
   cluster_sync();                                        // no block leaves while its sums are read
   if (threadIdx.x == 0 && stop) atomicAdd(&g_gave_up, 1u);
@@ -662,6 +747,9 @@ constexpr int64_t kMostIn8 = 131071, kMost = (1ll << 30) - 1;
 tcq_status_t check_sizes(int64_t n_tok, int64_t n_out, int64_t n_in, int64_t most_in) {
   if (n_tok < 0 || n_out <= 0 || n_in <= 0) return TCQ_ERR_INVALID_ARG;
   if (n_tok > kMost || n_out > kMost || n_in > most_in) return TCQ_ERR_UNSUPPORTED;
+  // tiles of 256 x 128, two products, halved: counted in 32 bits
+  const int64_t t = (n_tok >> 8) + 1, o = (n_out >> 7) + 1, i = (n_in >> 7) + 1;
+  if (t * o > kMost / 4 || t * i > kMost / 4 || o * i > kMost / 4) return TCQ_ERR_UNSUPPORTED;
   return TCQ_OK;
 }
 
@@ -732,25 +820,73 @@ int band_of(const Job &j) {
 // launch (elementwise pass counted), grad_x alone 300, the weights' two alone 288;
 // gated block 3001 x 2048 x 8192 (768 tiles, 74 clusters) 169.6 us in whole tiles,
 // 168.9 with the last 28 halved (power, not the idle SMs, sets the time there).
+int clusters_of_gpu() { return std::max(1, sm_count() / 2); }
+
+// Parts of the contraction for `count` tiles of `steps` steps whose sums are `sums`
+// bytes: the number, of those that the clusters hold at once with eight steps or
+// more each, that takes the least time by what was measured: 0.26 us a step while
+// few clusters run, 3 us to join and the parts' sums twice through L2 at 6 TB/s.
+// Measured (us, whole / best split): int8 129 x 8192 x 1024 25.4 / 13.7 (eight
+// parts), 1024 tokens 26.7 / 19.6 (four); 129 x 8192 x 2048 26.2 / 16.1 (four);
+// not split 129 x 2048 x 2048 10.8 / 12.5 (two), 1024 x 8192 x 2048 27.4 / 27.7.
+int parts_of(int64_t count, int64_t steps, double sums) {
+  const int64_t most = std::min<int64_t>(clusters_of_gpu() / std::max<int64_t>(1, count), steps / 8);
+  int best = 1;
+  double least = 0.26 * (double)steps;
+  for (int64_t s = 2; s <= most; ++s) {
+    const double t = 0.26 * (double)steps / (double)s + 3.0 + 2.0 * (double)s * sums / 6e6;
+    if (t < least) {
+      least = t;
+      best = (int)s;
+    }
+  }
+  return best;
+}
+
+// A job's tiles and parts; what its parts' sums take in the workspace.
+struct Plan {
+  int mt, nt, split;
+  int64_t pitch;
+  size_t bytes;
+};
+Plan plan_of(int64_t M, int64_t N, int cols, int z, int planes, int64_t steps) {
+  Plan l;
+  l.mt = (int)tiles(M, 256);
+  l.nt = (int)tiles(N, cols);
+  l.pitch = round_up(N, 16);
+  l.split = parts_of((int64_t)l.mt * l.nt * z, steps, 4.0 * planes * (double)M * (double)l.pitch);
+  l.bytes = l.split > 1 ? round256((size_t)l.split * planes * M * l.pitch * 4) : 0;
+  return l;
+}
+
+void lay_out(Job &j, const Plan &l, Workspace &w) {
+  j.mt = l.mt;
+  j.nt = l.nt;
+  j.split = l.split;
+  j.pitch = l.pitch;
+  j.part = l.bytes ? (float *)w.take(l.bytes) : nullptr;
+}
+
 void deal(PairParams &p, int jobs, int clusters) {
   p.shares = 0;
   for (int i = 0; i < jobs; ++i) p.job[i].band = band_of(p.job[i]);
   const auto give = [&](int job, int64_t first, int64_t n, int narrow, int64_t lo, int64_t hi) {
-    if (hi > lo) p.share[p.shares++] = {job, (int)first, (int)n, narrow, lo, hi};
+    if (hi > lo) p.share[p.shares++] = {job, (int)first, (int)n, narrow, (uint32_t)lo, (uint32_t)hi};
   };
-  const auto count = [&](int j) { return (int64_t)p.job[j].mt * p.job[j].nt * p.job[j].z; };
+  const auto count = [&](int j) { return (int64_t)p.job[j].mt * p.job[j].nt * p.job[j].z * p.job[j].split; };
   const auto finish = [&](int j, int64_t lo) {
     const int64_t hi = count(j), rest = (hi - lo) % clusters;
-    const bool halve = rest > 0 && 2 * rest <= clusters;
+    const bool halve = rest > 0 && 2 * rest <= clusters && p.job[j].split == 1;
     give(j, 0, clusters, 0, lo, halve ? hi - rest : hi);
     if (halve) give(j, 0, clusters, 1, 2 * (hi - rest), 2 * hi);
   };
   if (jobs == 1) return finish(0, 0);
   int64_t cost[2];
-  for (int j = 0; j < 2; ++j) cost[j] = (int64_t)p.job[j].kb * p.job[j].segs;
+  for (int j = 0; j < 2; ++j)                            // a tile's write-out takes as long as eight steps
+    cost[j] = p.job[j].kb * p.job[j].segs / p.job[j].split + 8;
   const int big = cost[0] >= cost[1] ? 0 : 1, small = 1 - big;
   int64_t t = count(big), c = cost[big];
-  const bool halve = 2 * t <= clusters;
+  const bool halve = 2 * t <= clusters && p.job[big].split == 1;
   if (halve) {
     t *= 2;
     c = (c + 1) / 2;
@@ -767,13 +903,26 @@ tcq_status_t launch_pair(PairParams &p, int jobs, cudaStream_t s) {
   if (cudaFuncSetAttribute(pair_kernel<I8, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) !=
       cudaSuccess)
     return TCQ_ERR_CUDA;
-  const int clusters = std::max(1, sm_count() / 2);
-  deal(p, jobs, clusters);
+  deal(p, jobs, clusters_of_gpu());
   int64_t grid = 0;                                      // clusters that get a tile
   for (int i = 0; i < p.shares; ++i)
-    grid = std::max<int64_t>(grid, p.share[i].first + std::min<int64_t>(p.share[i].n, p.share[i].hi - p.share[i].lo));
-  return launch(pair_kernel<I8, DUAL>, dim3(2 * (unsigned)grid), kPairThreads, kPairSmem, 0, s, p);
+    grid = std::max<int64_t>(grid, p.share[i].first + std::min<int64_t>(p.share[i].n, (int64_t)p.share[i].hi - p.share[i].lo));
+  tcq_status_t st = launch(pair_kernel<I8, DUAL>, dim3(2 * (unsigned)grid), kPairThreads, kPairSmem, 0, s, p);
+  for (int i = 0; i < jobs && st == TCQ_OK; ++i) {
+    const Job &j = p.job[i];
+    if (j.split == 1) continue;
+    const Join q = {j.part, j.split, j.planes, j.N % 4 == 0, j.M, j.N, j.pitch, {j.out[0], j.out[1]}, p.e};
+    st = launch(join_kernel<I8, DUAL>, dim3(blocks_for(j.M * tiles(j.N, 4)), 1, (unsigned)j.z), 256, 0, 0, s, q);
+  }
+  return st;
 }
+
+// Which kernel: up to 64 tokens (128 of a single product) rows_kernel.  Measured,
+// us, rows / pair: int8 8192 x 8192 at 64 tokens 17.1 / 24.0, 128 21.2 / 25.1, 256
+// 29.3 / 26.7; bf16 gated block 2048 -> 8192 at 64 17.6 / 19.3, 96 19.6 / 19.8, 128
+// 21.5 / 20.4; int8 gated block at 64 13.3 / 14.3, 96 15.6 / 14.6.
+template <bool DUAL>
+bool few_tokens(int64_t M) { return M <= (DUAL ? 64 : 128); }
 
 template <bool I8, bool DUAL, int NT>
 tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
@@ -795,26 +944,37 @@ extern "C" tcq_status_t tcq_products_gave_up(unsigned int *count) {
   return cudaMemcpyFromSymbol(count, g_gave_up, sizeof(unsigned)) == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA;
 }
 
+// What a forward product needs: operands at an aligned pitch, the parts' sums.
+template <bool DUAL>
+static size_t product_bytes(int64_t M, int64_t N, int64_t K, int es) {
+  return pitch_bytes(M, K * es) + (DUAL ? 2 : 1) * pitch_bytes(N, K * es) +
+         (few_tokens<DUAL>(M) ? 0 : plan_of(M, N, DUAL ? 128 : 256, 1, DUAL ? 2 : 1, tiles(K * es, 128)).bytes);
+}
+
 extern "C" size_t tcq_int8_matmul_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
   if (check_sizes(n_tok, n_out, n_in, kMostIn8) != TCQ_OK) return 0;
-  return pitch_bytes(n_tok, n_in) + pitch_bytes(n_out, n_in);
+  return product_bytes<false>(n_tok, n_out, n_in, 1);
 }
 
 extern "C" size_t tcq_int8_gated_ffn_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
   if (check_sizes(n_tok, n_out, n_in, kMostIn8) != TCQ_OK) return 0;
-  return pitch_bytes(n_tok, n_in) + 2 * pitch_bytes(n_out, n_in);
+  return product_bytes<true>(n_tok, n_out, n_in, 1);
 }
 
 extern "C" size_t tcq_gated_ffn_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
   if (check_sizes(n_tok, n_out, n_in, kMost) != TCQ_OK) return 0;
-  return pitch_bytes(n_tok, 2 * n_in) + 2 * pitch_bytes(n_out, 2 * n_in);
+  return product_bytes<true>(n_tok, n_out, n_in, 2);
 }
 
-// dg and du; x, Wg and Wu where their rows need an aligned pitch
+static Plan plan_grad_x(int64_t M, int64_t F, int64_t K) { return plan_of(M, K, 256, 1, 1, 2 * tiles(F, 64)); }
+static Plan plan_grad_w(int64_t M, int64_t F, int64_t K, int z) { return plan_of(F, K, 256, z, z, tiles(M, 64)); }
+
+// dg and du; x, Wg and Wu where their rows need an aligned pitch; the parts' sums
 extern "C" size_t tcq_gated_ffn_backward_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
   if (check_sizes(n_tok, n_out, n_in, kMost) != TCQ_OK) return 0;
   return 2 * round256((size_t)n_tok * round_up(2 * n_out, 16)) + pitch_bytes(n_tok, 2 * n_in) +
-         2 * pitch_bytes(n_out, 2 * n_in);
+         2 * pitch_bytes(n_out, 2 * n_in) + plan_grad_x(n_tok, n_out, n_in).bytes +
+         std::max(plan_grad_w(n_tok, n_out, n_in, 1).bytes, plan_grad_w(n_tok, n_out, n_in, 2).bytes);
 }
 
 static bool no_workspace(const void *ws, size_t have, size_t need) {
@@ -830,7 +990,7 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
   tcq_status_t st = ready(A, a, M, K, es, w, s);
   for (int i = 0; i < (DUAL ? 2 : 1) && st == TCQ_OK; ++i) st = ready(B[i], i ? w1 : w0, N, K, es, w, s);
   if (st != TCQ_OK) return st;
-  if (M <= 128) {
+  if (few_tokens<DUAL>(M)) {
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     RowsParams r;
     if (!map_of(&r.w[0], B[0], 128) || (DUAL && !map_of(&r.w[1], B[1], 128)) || !map_of(&r.x, A, nt))
@@ -844,8 +1004,8 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
     r.e = e;
     return nt == 16   ? launch_rows<I8, DUAL, 16>(r, s)
            : nt == 32 ? launch_rows<I8, DUAL, 32>(r, s)
-           : nt == 64 ? launch_rows<I8, DUAL, 64>(r, s)
-                      : launch_rows<I8, DUAL, 128>(r, s);
+           : DUAL || nt == 64 ? launch_rows<I8, DUAL, 64>(r, s)
+                              : launch_rows<I8, false, 128>(r, s);
   }
   PairParams p;
   p.bf16 = bf16;
@@ -857,9 +1017,9 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
   j.out[0] = out;
   j.M = M;
   j.N = N;
-  j.mt = (int)tiles(M, 256);
-  j.nt = (int)tiles(N, DUAL ? 128 : 256);
   j.kb = (int)tiles(K * es, 128);
+  j.planes = DUAL ? 2 : 1;
+  lay_out(j, plan_of(M, N, DUAL ? 128 : 256, 1, j.planes, j.kb), w);
   j.segs = 1;
   j.z = 1;
   j.a_mn = j.b_mn = 0;
@@ -969,6 +1129,8 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
     j.z = 1;
     j.a_mn = 0;
     j.wide = width(grad_x, n_in, 2);
+    j.planes = 1;
+    lay_out(j, plan_grad_x(n_tok, n_out, n_in), w);
   }
   if (grad_w_gate || grad_w_up) {
     // dg^T x and du^T x: both operands' rows (tokens) run along the sum
@@ -989,13 +1151,13 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
     j.kb = (int)tiles(n_tok, 64);
     j.segs = 1;
     j.a_mn = 1;
+    j.planes = j.z;
+    lay_out(j, plan_grad_w(n_tok, n_out, n_in, j.z), w);
   }
   for (int i = 0; i < jobs; ++i) {
     Job &j = p.job[i];
     j.N = n_in;
     j.b_mn = 1;
-    j.mt = (int)tiles(j.M, 256);
-    j.nt = (int)tiles(n_in, 256);
   }
   return launch_pair<false, false>(p, jobs, s);
 }
