@@ -24,7 +24,8 @@
 namespace tcq {
 
 constexpr int kStages = 6, kStageBytes = 32768, kPairThreads = 320;
-constexpr int kPairSmem = kStages * kStageBytes + 1024;
+// the ring, and 32 rows of 16 + 1 values for each of the eight epilogue warps
+constexpr int kStagePitch = 17, kPairSmem = kStages * kStageBytes + 8 * 32 * kStagePitch * 4 + 1024;
 
 // One product: sums over `segs` pairs of operands a[s], b[s] in turn, or (z > 1)
 // z products with operands a[z] and the same b[0].
@@ -140,35 +141,51 @@ __device__ __forceinline__ void store_words(char *p, const uint32_t (&v)[8], int
   }
 }
 
-// Sixteen neighbouring results of one row, the first `n` of them inside the matrix.
-__device__ __forceinline__ void store16(void *out, int64_t at, int dtype, const float (&v)[16], int n, int wide) {
-  if (n >= 16 && wide >= 16) {
-    uint32_t w[8];
-    if (dtype == TCQ_F32) {
+// Sixteen neighbouring results of one row (`wide` 16 or 32: bytes of a store).
+__device__ __forceinline__ void store16(void *out, int64_t at, int dtype, const float (&v)[16], int wide) {
+  uint32_t w[8];
+  if (dtype == TCQ_F32) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
-        store_words((char *)out + 4 * at + 32 * h, w, wide);
-      }
-    } else {
-      if (dtype == TCQ_F16) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], TCQ_F16);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], TCQ_BF16);
-      }
-      store_words((char *)out + 2 * at, w, wide);
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+      store_words((char *)out + 4 * at + 32 * h, w, wide);
     }
     return;
   }
+  if (dtype == TCQ_F16) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (i >= n) continue;
-    if (dtype == TCQ_F32) ((float *)out)[at + i] = v[i];
-    else ((uint16_t *)out)[at + i] = (uint16_t)pack2(v[i], 0.0f, dtype);
+    for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], TCQ_F16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], TCQ_BF16);
   }
+  store_words((char *)out + 2 * at, w, wide);
+}
+
+// The same for a whole warp's 32 rows where rows start anywhere or the matrix
+// ends inside the sixteen: through shared memory, so that half a warp writes
+// neighbouring values of one row (element stores of a lane's own row would touch
+// 32 sectors each: the gated block 777 x 1024 x 2731 took 53 us so, STAGED_US this way).
+__device__ __noinline__ void store_rows(const float *buf, void *out, int64_t at, int rows, int64_t N, int valid,
+                                        int dtype) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  if (c >= valid) return;
+#pragma unroll 4
+  for (int r = lane >> 4; r < rows; r += 2) {
+    const float x = buf[r * kStagePitch + c];
+    const int64_t to = at + r * N + c;
+    if (dtype == TCQ_F32) ((float *)out)[to] = x;
+    else ((uint16_t *)out)[to] = (uint16_t)pack2(x, 0.0f, dtype);
+  }
+}
+__device__ __forceinline__ void store16_staged(float *buf, void *out, int64_t row0, int64_t M, int64_t N, int64_t ch,
+                                               int valid, int dtype, const float (&v)[16]) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) buf[(threadIdx.x & 31) * kStagePitch + i] = v[i];
+  __syncwarp();
+  store_rows(buf, out, row0 * N + ch, (int)max((int64_t)0, min((int64_t)32, M - row0)), N, valid, dtype);
 }
 
 // Sixteen channels' scales (or biases) from channel n on, `valid` of them there.
@@ -318,6 +335,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp >= 2) {
     // ---- results: warp w reads the lanes of quarter w % 4, one half of the columns
     const int quarter = warp & 3, half = (warp - 2) >> 2;
+    float *stage = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)) + kStages * kStageBytes) +
+                   (warp - 2) * 32 * kStagePitch;
     int n_acc = 0;
     Tiles it;
     while (it.next(p, cluster)) {
@@ -348,20 +367,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         const int64_t ch = n0 + 16 * c;
         const int valid = (int)min((int64_t)16, j.N - ch);
-        if (!in || valid <= 0) continue;
+        if (valid <= 0) continue;
         if (j.split > 1) {
+          if (!in) continue;
           float *part = j.part + (((int64_t)at.s * j.planes + (DUAL ? 0 : at.z)) * j.M + row) * j.pitch + ch;
-          store16(part, 0, TCQ_F32, g, 16, 32);
-          if (DUAL) store16(part + j.M * j.pitch, 0, TCQ_F32, u, 16, 32);
+          store16(part, 0, TCQ_F32, g, 32);
+          if (DUAL) store16(part + j.M * j.pitch, 0, TCQ_F32, u, 32);
           continue;
         }
-        const int64_t to = row * j.N + ch;
+        const int64_t to = row * j.N + ch, row0 = row - lane;
         finish16<I8>(g, p.e.s0, ch, valid, sa);
         if (DUAL) {
           finish16<I8>(u, p.e.s1, ch, valid, sa);
           if (!I8 && p.e.gate) {
-            store16(p.e.gate, to, TCQ_F32, g, valid, p.e.wide_save);
-            store16(p.e.up, to, TCQ_F32, u, valid, p.e.wide_save);
+            if (valid == 16 && p.e.wide_save >= 16) {
+              if (in) {
+                store16(p.e.gate, to, TCQ_F32, g, p.e.wide_save);
+                store16(p.e.up, to, TCQ_F32, u, p.e.wide_save);
+              }
+            } else {
+              store16_staged(stage, p.e.gate, row0, j.M, j.N, ch, valid, TCQ_F32, g);
+              store16_staged(stage, p.e.up, row0, j.M, j.N, ch, valid, TCQ_F32, u);
+            }
           }
           gate(g, u, p.e.act);
         } else if (I8 && p.e.bias) {
@@ -370,7 +397,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) g[i] = __fadd_rn(g[i], b[i]);
         }
-        store16(j.out[at.z], to, p.e.dtype, g, valid, j.wide);
+        if (valid == 16 && j.wide >= 16) {
+          if (in) store16(j.out[at.z], to, p.e.dtype, g, j.wide);
+        } else {
+          store16_staged(stage, j.out[at.z], row0, j.M, j.N, ch, valid, p.e.dtype, g);
+        }
       }
       ++n_acc;
     }
