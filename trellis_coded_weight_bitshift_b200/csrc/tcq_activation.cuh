@@ -32,12 +32,26 @@ __device__ __forceinline__ void activation_slope(float v, int act, float &a, flo
   }
 }
 
+// The activation of two values at once, times u: pairs where the hardware has them.
 template <int ACT>
-__device__ __forceinline__ float activation(float v) {
-  if (ACT == TCQ_ACT_SILU) return v * logistic(v);
-  if (ACT == TCQ_ACT_GELU) return 0.5f * v * erfcf(-0.70710678f * v);
-  if (ACT == TCQ_ACT_GELU_TANH) return v * logistic(1.59576912f * v * (1.0f + 0.044715f * v * v));
-  return v < 0.0f ? 0.0f : v;
+__device__ __forceinline__ f2_t gated_pair(f2_t g, f2_t u) {
+  if (ACT == TCQ_ACT_SILU || ACT == TCQ_ACT_GELU_TANH) {
+    // g * logistic(z), z = g or 2 sqrt(2/pi) (g + 0.044715 g^3); t = -z log2(e)
+    f2_t t;
+    if (ACT == TCQ_ACT_SILU) {
+      t = f2mul(g, f2(-1.44269504f, -1.44269504f));
+    } else {
+      const f2_t w = f2fma(f2mul(g, g), f2(-0.10294324f, -0.10294324f), f2(-2.30220820f, -2.30220820f));
+      t = f2mul(g, w);
+    }
+    const f2_t d = f2add(f2(ex2(f2lo(t)), ex2(f2hi(t))), f2(1.0f, 1.0f));
+    return f2mul(f2mul(g, f2(rcp(f2lo(d)), rcp(f2hi(d)))), u);
+  }
+  if (ACT == TCQ_ACT_GELU) {
+    const f2_t p = f2(erfcf(-0.70710678f * f2lo(g)), erfcf(-0.70710678f * f2hi(g)));
+    return f2mul(f2mul(f2mul(g, f2(0.5f, 0.5f)), p), u);
+  }
+  return f2mul(f2(f2lo(g) < 0.0f ? 0.0f : f2lo(g), f2hi(g) < 0.0f ? 0.0f : f2hi(g)), u);
 }
 
 // g = act(g) * u, N values.  One branch for all of them: a branch for each value
@@ -46,7 +60,11 @@ __device__ __forceinline__ float activation(float v) {
 template <int ACT, int N>
 __device__ __forceinline__ void gate_as(float (&g)[N], const float (&u)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) g[i] = activation<ACT>(g[i]) * u[i];
+  for (int i = 0; i < N; i += 2) {
+    const f2_t r = gated_pair<ACT>(f2(g[i], g[i + 1]), f2(u[i], u[i + 1]));
+    g[i] = f2lo(r);
+    g[i + 1] = f2hi(r);
+  }
 }
 template <int N>
 __device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int act) {

@@ -209,7 +209,12 @@ __device__ __forceinline__ void finish16(float (&v)[16], const float *s, int64_t
   float c[16];
   channel16(s, n, valid, c);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = (float)__float_as_int(v[i]) * sa * c[i];
+  for (int i = 0; i < 16; i += 2) {
+    const f2_t r = f2mul(f2mul(f2((float)__float_as_int(v[i]), (float)__float_as_int(v[i + 1])), f2(sa, sa)),
+                         f2(c[i], c[i + 1]));
+    v[i] = f2lo(r);
+    v[i + 1] = f2hi(r);
+  }
 }
 
 template <bool I8, bool DUAL>
