@@ -471,6 +471,27 @@ def _ffn_operands(x, w_gate, w_up):
     return n_tok, w_gate.shape[0], n_in
 
 
+def _launch_ffn(x, w_gate, w_up, act, sizes, out, gate, up, workspace):
+    """gated_ffn on checked operands; gate and up: addresses, 0 for none."""
+    need = int(lib().tcq_gated_ffn_workspace_size(*sizes))
+    ws = _use_workspace(workspace, need, x) if need else None
+    check(lib().tcq_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _DTYPE[x.dtype], *sizes, int(act),
+                              _ptr(out), gate, up, _ptr(ws), _nbytes(ws) if need else 0, _stream()),
+          "tcq_gated_ffn")
+
+
+def _launch_ffn_backward(x, w_gate, w_up, gate, up, grad_out, act, sizes, need, workspace):
+    """gated_ffn_backward on checked operands; gate and up: addresses."""
+    grads = [torch.empty_like(t) if n else None for t, n in zip((x, w_gate, w_up), need)]
+    size = int(lib().tcq_gated_ffn_backward_workspace_size(*sizes))
+    ws = _use_workspace(workspace, size, x)
+    check(lib().tcq_gated_ffn_backward(_ptr(x), _ptr(w_gate), _ptr(w_up), gate, up, _ptr(grad_out),
+                                       _DTYPE[x.dtype], *sizes, int(act), _ptr(grads[0]),
+                                       _ptr(grads[1]), _ptr(grads[2]), _ptr(ws), _nbytes(ws),
+                                       _stream()), "tcq_gated_ffn_backward")
+    return tuple(grads)
+
+
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: int = ACT_SILU,
               out: torch.Tensor | None = None, save: bool = False,
               workspace: torch.Tensor | None = None):
@@ -478,16 +499,12 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: in
     n_in] and weights [n_out, n_in], sums and activation in fp32.  With
     ``save=True`` returns (h, gate, up), the fp32 projections that
     ``gated_ffn_backward`` takes."""
-    n_tok, n_out, n_in = _ffn_operands(x, w_gate, w_up)
-    out = _result(out, (n_tok, n_out), x.dtype, x)
+    sizes = _ffn_operands(x, w_gate, w_up)
+    out = _result(out, sizes[:2], x.dtype, x)
     gate = up = None
     if save:
-        gate, up = (torch.empty(n_tok, n_out, dtype=torch.float32, device=x.device) for _ in range(2))
-    need = int(lib().tcq_gated_ffn_workspace_size(n_tok, n_out, n_in))
-    ws = _use_workspace(workspace, need, x) if need else None
-    check(lib().tcq_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _DTYPE[x.dtype], n_tok, n_out, n_in,
-                              int(act), _ptr(out), _ptr(gate), _ptr(up), _ptr(ws),
-                              _nbytes(ws) if need else 0, _stream()), "tcq_gated_ffn")
+        gate, up = (torch.empty(*sizes[:2], dtype=torch.float32, device=x.device) for _ in range(2))
+    _launch_ffn(x, w_gate, w_up, act, sizes, out, _ptr(gate), _ptr(up), workspace)
     return (out, gate, up) if save else out
 
 
@@ -498,20 +515,14 @@ def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
     """Gradients of ``gated_ffn`` for the output gradient ``grad_out`` and the
     saved ``gate`` and ``up``; returns (grad_x, grad_w_gate, grad_w_up), None
     where ``need`` is false."""
-    n_tok, n_out, n_in = _ffn_operands(x, w_gate, w_up)
+    sizes = _ffn_operands(x, w_gate, w_up)
     _require_cuda(x, gate, up, grad_out)
-    if any(t.shape != (n_tok, n_out) or t.dtype != torch.float32 for t in (gate, up)):
-        raise ValueError(f"gate and up must be float32 tensors [{n_tok}, {n_out}]")
-    if grad_out.shape != (n_tok, n_out) or grad_out.dtype != x.dtype:
-        raise ValueError(f"grad_out must be a {x.dtype} tensor [{n_tok}, {n_out}]")
-    grads = [torch.empty_like(t) if n else None for t, n in zip((x, w_gate, w_up), need)]
-    size = int(lib().tcq_gated_ffn_backward_workspace_size(n_tok, n_out, n_in))
-    ws = _use_workspace(workspace, size, x)
-    check(lib().tcq_gated_ffn_backward(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up),
-                                       _ptr(grad_out), _DTYPE[x.dtype], n_tok, n_out, n_in, int(act),
-                                       _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]), _ptr(ws),
-                                       _nbytes(ws), _stream()), "tcq_gated_ffn_backward")
-    return tuple(grads)
+    if any(t.shape != sizes[:2] or t.dtype != torch.float32 for t in (gate, up)):
+        raise ValueError(f"gate and up must be float32 tensors {list(sizes[:2])}")
+    if grad_out.shape != sizes[:2] or grad_out.dtype != x.dtype:
+        raise ValueError(f"grad_out must be a {x.dtype} tensor {list(sizes[:2])}")
+    return _launch_ffn_backward(x, w_gate, w_up, _ptr(gate), _ptr(up), grad_out, act, sizes, need,
+                                workspace)
 
 
 class GatedFfn(torch.autograd.Function):
@@ -525,17 +536,30 @@ class GatedFfn(torch.autograd.Function):
     def forward(ctx, x, w_gate, w_up, act=ACT_SILU):
         if not any(ctx.needs_input_grad[:3]):
             return gated_ffn(x, w_gate, w_up, act)
-        h, gate, up = gated_ffn(x, w_gate, w_up, act, save=True)
-        ctx.save_for_backward(x, w_gate, w_up, gate, up)
-        ctx.act = act
-        return h
+        sizes = _ffn_operands(x, w_gate, w_up)
+        out = _result(None, sizes[:2], x.dtype, x)
+        # both projections in one buffer, the second on a 16-byte boundary
+        half = (sizes[0] * sizes[1] + 3) // 4 * 4
+        saved = torch.empty(2 * half, dtype=torch.float32, device=x.device)
+        _launch_ffn(x, w_gate, w_up, act, sizes, out, _ptr(saved), _ptr(saved) + 4 * half, None)
+        ctx.save_for_backward(x, w_gate, w_up, saved)
+        ctx.act, ctx.sizes = act, sizes
+        return out
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_out):
+    def _gradients(ctx, grad_out):
+        x, w_gate, w_up, saved = ctx.saved_tensors
         grad_out = grad_out.contiguous()
         if grad_out.data_ptr() % 16:                 # a slice of a larger gradient may start anywhere
             grad_out = grad_out.clone()
-        grads = gated_ffn_backward(*ctx.saved_tensors, grad_out, ctx.act,
-                                   need=ctx.needs_input_grad[:3])
-        return (*grads, None)
+        _require_cuda(x, grad_out)
+        return (*_launch_ffn_backward(x, w_gate, w_up, _ptr(saved), _ptr(saved) + 2 * saved.numel(),
+                                      grad_out, ctx.act, ctx.sizes, ctx.needs_input_grad[:3], None),
+                None)
+
+    _once = staticmethod(torch.autograd.function.once_differentiable(_gradients.__func__))
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        # only a backward pass that builds a graph needs the guard against a second derivative
+        return (GatedFfn._once if torch.is_grad_enabled() else GatedFfn._gradients)(ctx, grad_out)

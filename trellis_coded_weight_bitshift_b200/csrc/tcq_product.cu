@@ -685,12 +685,23 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
 }
 
 // Rows of `bytes` bytes, packed, to rows `pitch` bytes apart (a multiple of 16),
-// 16 bytes a thread.  The source is read in whole aligned words; the last row's
-// end is read by bytes, so nothing past it is touched.
-__global__ void __launch_bounds__(256) pitch_rows_kernel(const uint8_t *__restrict__ src, int64_t rows, int64_t bytes,
-                                                         int64_t pitch, uint4 *__restrict__ dst) {
+// 16 bytes a thread; blockIdx.y: the matrix.  The source is read in whole aligned
+// words; the last row's end is read by bytes, so nothing past it is touched.
+struct PitchCopies {
+  struct {
+    const uint8_t *src;
+    int64_t rows, bytes, pitch;
+    uint4 *dst;
+  } m[3];
+  int n;
+};
+__global__ void __launch_bounds__(256) pitch_rows_kernel(const PitchCopies p) {
   after_previous();
   let_next_start();
+  const auto &c0 = p.m[blockIdx.y];
+  const uint8_t *__restrict__ src = c0.src;
+  uint4 *__restrict__ dst = c0.dst;
+  const int64_t rows = c0.rows, bytes = c0.bytes, pitch = c0.pitch;
   const int64_t per = pitch >> 4, n = rows * per, total = rows * bytes;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per, c = (i - r * per) << 4;
@@ -827,13 +838,21 @@ struct Workspace {
   }
 };
 
-tcq_status_t ready(Operand &o, const void *p, int64_t rows, int64_t cols, int es, Workspace &ws, cudaStream_t s) {
-  o = {p, rows, cols, round_up(cols * es, 16), es};
-  if (!needs_pitch(rows, cols * es)) return TCQ_OK;
+// Copies to an aligned pitch, collected and then made in one launch.
+Operand ready(const void *p, int64_t rows, int64_t cols, int es, Workspace &ws, PitchCopies &todo) {
+  Operand o = {p, rows, cols, round_up(cols * es, 16), es};
+  if (!needs_pitch(rows, cols * es)) return o;
   uint4 *copy = (uint4 *)ws.take(pitch_bytes(rows, cols * es));
+  todo.m[todo.n++] = {(const uint8_t *)p, rows, cols * es, o.pitch, copy};
   o.p = copy;
-  return launch(pitch_rows_kernel, dim3(blocks_for(rows * (o.pitch / 16))), 256, 0, 0, s, (const uint8_t *)p, rows,
-                cols * es, o.pitch, copy);
+  return o;
+}
+
+tcq_status_t make_copies(const PitchCopies &todo, cudaStream_t s) {
+  if (todo.n == 0) return TCQ_OK;
+  int64_t most = 0;
+  for (int i = 0; i < todo.n; ++i) most = std::max(most, todo.m[i].rows * (todo.m[i].pitch / 16));
+  return launch(pitch_rows_kernel, dim3(blocks_for(most), (unsigned)todo.n), 256, 0, 0, s, todo);
 }
 
 bool map_of(CUtensorMap *m, const Operand &o, int box_rows) {
@@ -1022,9 +1041,11 @@ template <bool I8, bool DUAL>
 static tcq_status_t product(const void *a, const void *w0, const void *w1, int es, int bf16, int64_t M, int64_t N,
                             int64_t K, void *out, Epilogue e, void *ws, cudaStream_t s) {
   Workspace w = {(char *)ws};
-  Operand A, B[2];
-  tcq_status_t st = ready(A, a, M, K, es, w, s);
-  for (int i = 0; i < (DUAL ? 2 : 1) && st == TCQ_OK; ++i) st = ready(B[i], i ? w1 : w0, N, K, es, w, s);
+  PitchCopies copies;
+  copies.n = 0;
+  Operand A = ready(a, M, K, es, w, copies), B[2];
+  for (int i = 0; i < (DUAL ? 2 : 1); ++i) B[i] = ready(i ? w1 : w0, N, K, es, w, copies);
+  tcq_status_t st = make_copies(copies, s);
   if (st != TCQ_OK) return st;
   if (few_tokens<DUAL>(M)) {
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
@@ -1140,7 +1161,9 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
 
   Workspace w = {(char *)ws};
   const int64_t pitch = round_up(2 * n_out, 16);
-  Operand d[2], X, W[2];
+  PitchCopies copies;
+  copies.n = 0;
+  Operand d[2];
   for (Operand &o : d) o = {w.take((size_t)n_tok * pitch), n_tok, n_out, pitch, 2};
   st = dtype == TCQ_F16 ? gate_grads<__half>(grad_h, gate, up, n_tok, n_out, pitch, act, d[0].p, d[1].p, s)
                         : gate_grads<__nv_bfloat16>(grad_h, gate, up, n_tok, n_out, pitch, act, d[0].p, d[1].p, s);
@@ -1154,9 +1177,8 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
     // one sum over both halves: dg Wg, then du Wu; the weights' rows run along it
     Job &j = p.job[jobs++];
     for (int i = 0; i < 2; ++i) {
-      st = ready(W[i], i ? w_up : w_gate, n_out, n_in, 2, w, s);
-      if (st != TCQ_OK) return st;
-      if (!map_of(&j.a[i], d[i], 128) || !map_of(&j.b[i], W[i], 64)) return TCQ_ERR_CUDA;
+      const Operand W = ready(i ? w_up : w_gate, n_out, n_in, 2, w, copies);
+      if (!map_of(&j.a[i], d[i], 128) || !map_of(&j.b[i], W, 64)) return TCQ_ERR_CUDA;
     }
     j.out[0] = grad_x;
     j.M = n_tok;
@@ -1171,8 +1193,7 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
   if (grad_w_gate || grad_w_up) {
     // dg^T x and du^T x: both operands' rows (tokens) run along the sum
     Job &j = p.job[jobs++];
-    st = ready(X, x, n_tok, n_in, 2, w, s);
-    if (st != TCQ_OK) return st;
+    const Operand X = ready(x, n_tok, n_in, 2, w, copies);
     if (!map_of(&j.b[0], X, 64)) return TCQ_ERR_CUDA;
     j.z = 0;
     j.wide = 32;
@@ -1195,5 +1216,6 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
     j.N = n_in;
     j.b_mn = 1;
   }
-  return launch_pair<false, false>(p, jobs, s);
+  st = make_copies(copies, s);
+  return st == TCQ_OK ? launch_pair<false, false>(p, jobs, s) : st;
 }
