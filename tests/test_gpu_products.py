@@ -176,7 +176,8 @@ def test_decode_int8_tiles(tcq, L, layout, rows, cols):
 SIZES = [(1, 1, 1), (1, 8, 16), (1, 256, 4096), (2, 17, 16), (3, 100, 33), (15, 129, 128), (16, 128, 256),
          (17, 127, 1000), (33, 64, 1024), (48, 520, 48), (64, 300, 2048), (65, 257, 160), (100, 1000, 127),
          (127, 128, 64), (128, 256, 128), (129, 256, 144), (200, 96, 8192), (255, 513, 96), (256, 1024, 1024),
-         (257, 240, 31), (300, 511, 272), (777, 1041, 640)]
+         (257, 240, 31), (300, 511, 272), (777, 1041, 640), (129, 250, 8192), (300, 96, 5000), (1000, 2100, 1500),
+         (1, 20000, 65)]
 
 
 def _int8(g, *shape):
@@ -244,7 +245,10 @@ def test_int8_gated_ffn(tcq, M, N, K, act, dtype):
 
 # ------------------------------------------------------------ gated block
 
-FFN_SIZES = SIZES + [(1, 1000, 2048), (5, 8192, 64), (512, 384, 520)]
+# after these: one token, a very long and a very wide matrix; few tiles and a long sum (split over
+# clusters) of the block, of grad_x and of the weights' gradients; half tiles in the last round
+FFN_SIZES = SIZES + [(1, 1000, 2048), (5, 8192, 64), (512, 384, 520), (3, 20, 100000), (70, 260, 4100),
+                     (140, 4100, 264), (129, 8200, 40), (5000, 200, 136), (700, 2500, 130), (2, 30000, 24)]
 
 
 def _ffn_inputs(seed, M, N, K, dtype):
@@ -379,6 +383,83 @@ def test_autograd_takes_any_gradient_layout(tcq):
     (g,) = torch.autograd.grad(y.sum(), xr, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+def test_a_long_sum_of_equal_signs(tcq):
+    # nothing cancels: an accumulator that lost low bits would show at once
+    x = torch.full((4, 60000), 0.5, dtype=F16, device="cuda")
+    w = torch.full((24, 60000), 2.0 ** -11, dtype=F16, device="cuda")
+    h, gate, up = tcq.gated_ffn(x, w, w, act=tcq.ACT_RELU, save=True)
+    want = 60000 * 0.5 * 2.0 ** -11
+    assert bool((gate == want).all()) and bool((up == want).all())         # exact in fp32
+    assert bool((h.double() - want * want).abs().max() <= want * want * 2.0 ** -11)
+
+
+@pytest.mark.parametrize("N,K", [(200, 136), (77, 61)])
+def test_int8_results_do_not_depend_on_the_batch(tcq, N, K):
+    g = _gen(8)
+    a, sa, w, sw, b = _int8(g, 400, K), _pos(g, 400), _int8(g, N, K), _pos(g, N), _randn(g, N)
+    every = tcq.int8_matmul(a, sa, w, sw, bias=b, out_dtype=F32)
+    for lo, hi in ((0, 1), (7, 20), (100, 160), (3, 130), (0, 257)):
+        part = tcq.int8_matmul(a[lo:hi].clone(), sa[lo:hi].clone(), w, sw, bias=b, out_dtype=F32)
+        assert torch.equal(part, every[lo:hi])
+
+
+def test_offsets_past_32_bits(tcq):
+    # more than 2^31 values in and out; the last rows, and some in between, against the definition
+    rows, cols = 262200, 8200
+    x = torch.empty(rows, cols, dtype=F16, device="cuda")
+    pick = torch.tensor([0, 1, 130000, 261900, rows - 2, rows - 1], device="cuda")
+    x[:] = torch.randn(cols, device="cuda", generator=_gen(1)).half()
+    x[pick] = _randn(_gen(2), 6, cols).half()
+    q, s = tcq.quantize_int8(x)
+    rq, rs = _quantize_ref(x[pick])
+    assert torch.equal(q[pick], rq) and torch.equal(s[pick], rs)
+    del x
+    w, sw = _int8(_gen(3), 48, cols), _pos(_gen(4), 48)
+    y = tcq.int8_matmul(q, s, w, sw, out_dtype=F32)
+    p = (rq.double() @ w.double().t()) * rs.double()[:, None] * sw.double()
+    _within(y[pick], p, p.abs() * 4.01 * 2.0 ** -24)
+    del q, y
+    # results past 2^31: 65,700 tokens by 32,800 channels
+    M, N, K = 65700, 32800, 64
+    a, sa, w, sw = _int8(_gen(5), M, K), _pos(_gen(6), M), _int8(_gen(7), N, K), _pos(_gen(8), N)
+    y = tcq.int8_matmul(a, sa, w, sw, out_dtype=BF16)
+    r = torch.tensor([0, 255, 40000, M - 1], device="cuda")
+    p = (a[r].double() @ w.double().t()) * sa[r].double()[:, None] * sw.double()
+    _within(y[r], p, p.abs() * 4.01 * 2.0 ** -24 + _half_step(p, BF16) * 1.01)
+    del y
+    n = (1 << 23) + 40                               # streams of 256 weights
+    bits = torch.randint(0, 2 ** 31, (n, 16), device="cuda", generator=_gen(9), dtype=torch.int32).view(torch.uint32)
+    out = tcq.decode_int8(bits, 16)
+    assert out.numel() > 2 ** 31
+    assert torch.equal(out[-300:], tcq.decode_int8(bits[-300:].clone(), 16))
+    assert torch.equal(out[:300], tcq.decode_int8(bits[:300].clone(), 16))
+
+
+def test_training_step_captured_into_a_graph(tcq):
+    x, wg, wu, grad = _ffn_inputs(4, 140, 264, 96, BF16)
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu)]
+
+    def step():
+        h = tcq.GatedFfn.apply(*leaves, tcq.ACT_GELU)
+        return (h.detach(), *torch.autograd.grad(h, leaves, grad))
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_empty_batches(tcq):
@@ -576,3 +657,9 @@ def test_binding_refuses_misaligned_and_strided_operands(tcq):
         tcq.gated_ffn(off, wg, wu)
     with pytest.raises(ValueError):
         tcq.gated_ffn(x, wg.cpu(), wu)
+
+
+def test_no_wait_ever_ran_out(tcq):
+    x, wg, wu, _ = _ffn_inputs(1, 300, 300, 300, F16)
+    tcq.gated_ffn(x, wg, wu)
+    assert tcq.products_gave_up() == 0
