@@ -320,7 +320,8 @@ TCQ_API tcq_status_t tcq_rht(const float *W, int64_t rows, int64_t cols, const f
  * overflow).  Any other size is taken; n_in a multiple of
  * 16 bytes (8 elements of 16 bits, 16 of int8) spares a copy of the operands
  * into the workspace, n_out a multiple of 16 elements spares narrow stores.
- * Outputs may not overlap inputs.  `ws` is a device workspace of at least the
+ * Outputs and the workspace may not overlap inputs or one another (an invalid
+ * argument).  `ws` is a device workspace of at least the
  * matching *_workspace_size() bytes, 256-byte aligned (a size of 0 allows
  * NULL); nothing in it is kept between calls.
  * A value that is not finite spreads as in the formulas: an infinity or NaN

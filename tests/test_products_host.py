@@ -95,6 +95,37 @@ def test_backward_argument_combinations(L):
     assert L.tcq_int8_matmul(P, P, P, P, ctypes.c_void_p(260), 4, 8, 8, P, 0, P, BIG, None) == INV
 
 
+def test_outputs_may_not_overlap(L):
+    # every operand in its own megabyte, then the output moved onto each of them, and onto the workspace
+    def at(i, off=0):
+        return ctypes.c_void_p((i + 1) << 20 | off)
+    m, n, k = 200, 24, 40                                      # rows of 40 bytes: the workspace is in use
+    ws = at(20)
+    for onto in [at(i) for i in range(5)] + [at(0, m * k - 16), at(20), at(20, 256)]:
+        assert L.tcq_int8_matmul(at(0), at(1), at(2), at(3), at(4), m, n, k, onto, 0, ws, BIG, None) == INV, onto
+    for onto in [at(i) for i in range(6)] + [at(20)]:
+        assert L.tcq_int8_gated_ffn(at(0), at(1), at(2), at(3), at(4), at(5), m, n, k, 0, onto, 0, ws, BIG,
+                                    None) == INV
+    for h, g, u in ((at(0), None, None), (at(2), None, None), (at(5), at(5), at(6)), (at(5), at(6), at(6, 16)),
+                    (at(5), at(1), at(6))):
+        assert L.tcq_gated_ffn(at(0), at(1), at(2), 0, m, n, 41, 0, h, g, u, ws, BIG, None) == INV
+    for gx, g1, g2 in ((at(0), None, None), (None, at(1), None), (None, None, at(5)), (at(7), at(7), None),
+                       (None, at(8), at(8, 16)), (at(20), None, None)):
+        assert L.tcq_gated_ffn_backward(at(0), at(1), at(2), at(3), at(4), at(5), 0, m, n, k, 0, gx, g1, g2, ws, BIG,
+                                        None) == INV
+    assert L.tcq_quantize_int8(at(0), 0, m, k, at(0), at(1), None) == INV
+    assert L.tcq_quantize_int8(at(0), 0, m, k, at(1), at(1, m * k - 16), None) == INV
+    tr = ctypes.byref(_abi.trellis(16, 256))
+    assert L.tcq_decode_int8(tr, at(0), 4, 0, 0, 0, 0, at(0, 64), None) == INV
+
+
+def test_sizes_whose_tiles_pass_32_bits_are_refused(L):
+    big = 1 << 29
+    assert L.tcq_int8_matmul(P, P, P, P, None, big, big, 64, P, 0, P, BIG, None) == UNS
+    assert L.tcq_gated_ffn(P, P, P, 0, 64, big, big, 0, P, None, None, P, BIG, None) == UNS
+    assert L.tcq_gated_ffn_backward_workspace_size(big, 64, big) == 0
+
+
 def test_workspace_sizes_of_impossible_products_are_zero(L):
     for name in NAMES:
         size = getattr(L, f"tcq_{name}_workspace_size")
@@ -179,6 +210,7 @@ def test_binding_checks_shapes_and_types(no_launch, monkeypatch):
         lambda: tcq.quantize_int8(torch.zeros(4, 4, dtype=torch.float64)),
         lambda: tcq.int8_matmul(x, s, qw, sw), lambda: tcq.int8_matmul(q, s[:3], qw, sw),
         lambda: tcq.int8_matmul(q, s.double(), qw, sw), lambda: tcq.int8_matmul(q, s, qw[:, :16], sw),
+        lambda: tcq.int8_matmul(q, s, sw.to(torch.int8), sw), lambda: tcq.int8_matmul(q, s, sw[0].to(torch.int8), sw),
         lambda: tcq.int8_matmul(q, s, w, sw), lambda: tcq.int8_matmul(q, s, qw, sw[:7]),
         lambda: tcq.int8_matmul(q, s, qw, sw, bias=torch.zeros(7)),
         lambda: tcq.int8_matmul(q, s, qw, sw, bias=torch.zeros(8, **f16)),

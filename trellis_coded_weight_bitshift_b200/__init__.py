@@ -405,7 +405,7 @@ def _int8_operands(a, a_scale, weights, bias=None):
     if a.dim() != 2 or a.dtype != torch.int8:
         raise ValueError("a must be a 2-D int8 tensor [n_tok, n_in]")
     n_tok, n_in = a.shape
-    n_out = weights[0].shape[0]
+    n_out = weights[0].shape[0] if weights[0].dim() == 2 else -1
     for w, ws in zip(weights[::2], weights[1::2]):
         if w.dtype != torch.int8 or w.shape != (n_out, n_in):
             raise ValueError(f"weights must be int8 tensors of one shape [n_out, {n_in}]")

@@ -293,6 +293,8 @@ extern "C" tcq_status_t tcq_quantize_int8(const void *x, int dtype, int64_t rows
   if (!size_ok(rows) || !size_ok(cols)) return TCQ_ERR_UNSUPPORTED;
   if (rows == 0) return TCQ_OK;
   if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale)) return TCQ_ERR_INVALID_ARG;
+  const size_t n = (size_t)rows * cols;
+  if (clash({{q, n}, {scale, 4 * (size_t)rows}}, {{x, n * (dtype == TCQ_F32 ? 4 : 2)}})) return TCQ_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == TCQ_F16) return quantize_any((const __half *)x, rows, cols, q, scale, s);
   if (dtype == TCQ_BF16) return quantize_any((const __nv_bfloat16 *)x, rows, cols, q, scale, s);
@@ -334,6 +336,7 @@ extern "C" tcq_status_t tcq_decode_int8(const tcq_trellis_t *tr, const uint32_t 
   }
   if (n_seq == 0) return TCQ_OK;
   if (!bits || !out || !aligned16(bits) || !aligned16(out)) return TCQ_ERR_INVALID_ARG;
+  if (clash({{out, (size_t)n_seq * tr->seq_len}}, {{bits, 4 * wps * (size_t)n_seq}})) return TCQ_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   switch (tr->L) {
     case 8: return decode_launch<8>(tr, bits, n_seq, layout, tiles ? cols : 0, out, (int)wps, s);

@@ -10,6 +10,7 @@
 // 15.5 us a pass without, 13.6 with.
 #pragma once
 
+#include <initializer_list>
 #include <utility>
 
 #include "tcq_device.cuh"
@@ -22,6 +23,26 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 }  // namespace tcq
 
 namespace tcq_host {
+
+// What a call reads or writes.  `clash`: something written meets something read
+// or something else written (an empty range or NULL meets nothing).
+struct Range {
+  const void *p;
+  size_t n;
+};
+inline bool meet(const Range &a, const Range &b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && a.n && b.n && x < y + b.n && y < x + a.n;
+}
+inline bool clash(std::initializer_list<Range> out, std::initializer_list<Range> in) {
+  for (const Range *o = out.begin(); o != out.end(); ++o) {
+    for (const Range *q = o + 1; q != out.end(); ++q)
+      if (meet(*o, *q)) return true;
+    for (const Range &i : in)
+      if (meet(*o, i)) return true;
+  }
+  return false;
+}
 
 // cluster: blocks of a cluster along x (0: the kernel's own attribute, or none)
 template <typename... P, typename... A>

@@ -1093,7 +1093,11 @@ extern "C" tcq_status_t tcq_int8_matmul(const int8_t *a, const float *a_scale, c
   if (n_tok == 0) return TCQ_OK;
   if (bad_ptr(a) || bad_ptr(a_scale) || bad_ptr(w) || bad_ptr(w_scale) || bad_ptr(out) || !aligned16(bias))
     return TCQ_ERR_INVALID_ARG;
-  if (no_workspace(ws, ws_bytes, tcq_int8_matmul_workspace_size(n_tok, n_out, n_in))) return TCQ_ERR_WORKSPACE;
+  const size_t need = tcq_int8_matmul_workspace_size(n_tok, n_out, n_in), M = n_tok, N = n_out, K = n_in;
+  if (no_workspace(ws, ws_bytes, need)) return TCQ_ERR_WORKSPACE;
+  if (clash({{out, M * N * type_size(out_dtype)}, {ws, need}},
+            {{a, M * K}, {a_scale, 4 * M}, {w, N * K}, {w_scale, 4 * N}, {bias, 4 * N}}))
+    return TCQ_ERR_INVALID_ARG;
   const Epilogue e = {out_dtype, 0, a_scale, w_scale, nullptr, bias, nullptr, nullptr, 0};
   return product<true, false>(a, w, nullptr, 1, 0, n_tok, n_out, n_in, out, e, ws, (cudaStream_t)stream);
 }
@@ -1109,7 +1113,11 @@ extern "C" tcq_status_t tcq_int8_gated_ffn(const int8_t *a, const float *a_scale
   if (bad_ptr(a) || bad_ptr(a_scale) || bad_ptr(w_gate) || bad_ptr(w_gate_scale) || bad_ptr(w_up) ||
       bad_ptr(w_up_scale) || bad_ptr(h))
     return TCQ_ERR_INVALID_ARG;
-  if (no_workspace(ws, ws_bytes, tcq_int8_gated_ffn_workspace_size(n_tok, n_out, n_in))) return TCQ_ERR_WORKSPACE;
+  const size_t need = tcq_int8_gated_ffn_workspace_size(n_tok, n_out, n_in), M = n_tok, N = n_out, K = n_in;
+  if (no_workspace(ws, ws_bytes, need)) return TCQ_ERR_WORKSPACE;
+  if (clash({{h, M * N * type_size(out_dtype)}, {ws, need}},
+            {{a, M * K}, {a_scale, 4 * M}, {w_gate, N * K}, {w_gate_scale, 4 * N}, {w_up, N * K}, {w_up_scale, 4 * N}}))
+    return TCQ_ERR_INVALID_ARG;
   const Epilogue e = {out_dtype, act, a_scale, w_gate_scale, w_up_scale, nullptr, nullptr, nullptr, 0};
   return product<true, true>(a, w_gate, w_up, 1, 0, n_tok, n_out, n_in, h, e, ws, (cudaStream_t)stream);
 }
@@ -1124,7 +1132,11 @@ extern "C" tcq_status_t tcq_gated_ffn(const void *x, const void *w_gate, const v
   if (n_tok == 0) return TCQ_OK;
   if (bad_ptr(x) || bad_ptr(w_gate) || bad_ptr(w_up) || bad_ptr(h) || !aligned16(gate) || !aligned16(up))
     return TCQ_ERR_INVALID_ARG;
-  if (no_workspace(ws, ws_bytes, tcq_gated_ffn_workspace_size(n_tok, n_out, n_in))) return TCQ_ERR_WORKSPACE;
+  const size_t need = tcq_gated_ffn_workspace_size(n_tok, n_out, n_in), M = n_tok, N = n_out, K = n_in;
+  if (no_workspace(ws, ws_bytes, need)) return TCQ_ERR_WORKSPACE;
+  if (clash({{h, 2 * M * N}, {gate, 4 * M * N}, {up, 4 * M * N}, {ws, need}},
+            {{x, 2 * M * K}, {w_gate, 2 * N * K}, {w_up, 2 * N * K}}))
+    return TCQ_ERR_INVALID_ARG;
   Epilogue e = {dtype, act, nullptr, nullptr, nullptr, nullptr, gate, up, 0};
   e.wide_save = std::min(width(gate, n_out, 4), width(up, n_out, 4));
   return product<false, true>(x, w_gate, w_up, 2, dtype == TCQ_BF16, n_tok, n_out, n_in, h, e, ws,
@@ -1157,7 +1169,11 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
   if (bad_ptr(x) || bad_ptr(w_gate) || bad_ptr(w_up) || bad_ptr(gate) || bad_ptr(up) || bad_ptr(grad_h))
     return TCQ_ERR_INVALID_ARG;
   if (!grad_x && !grad_w_gate && !grad_w_up) return TCQ_OK;
-  if (no_workspace(ws, ws_bytes, tcq_gated_ffn_backward_workspace_size(n_tok, n_out, n_in))) return TCQ_ERR_WORKSPACE;
+  const size_t need = tcq_gated_ffn_backward_workspace_size(n_tok, n_out, n_in), M = n_tok, N = n_out, K = n_in;
+  if (no_workspace(ws, ws_bytes, need)) return TCQ_ERR_WORKSPACE;
+  if (clash({{grad_x, 2 * M * K}, {grad_w_gate, 2 * N * K}, {grad_w_up, 2 * N * K}, {ws, need}},
+            {{x, 2 * M * K}, {w_gate, 2 * N * K}, {w_up, 2 * N * K}, {gate, 4 * M * N}, {up, 4 * M * N}, {grad_h, 2 * M * N}}))
+    return TCQ_ERR_INVALID_ARG;
 
   Workspace w = {(char *)ws};
   const int64_t pitch = round_up(2 * n_out, 16);
