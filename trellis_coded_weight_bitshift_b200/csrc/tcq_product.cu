@@ -24,8 +24,10 @@
 namespace tcq {
 
 constexpr int kStages = 6, kStageBytes = 32768, kPairThreads = 320;
-// the ring, and 32 rows of 16 + 1 values for each of the eight epilogue warps
-constexpr int kStagePitch = 17, kPairSmem = kStages * kStageBytes + 8 * 32 * kStagePitch * 4 + 1024;
+// the ring; for each of the eight epilogue warps 32 rows of 16 + 1 values and two
+// scales (or a scale and a bias) for each of its 128 columns
+constexpr int kStagePitch = 17, kWarpFloats = 32 * kStagePitch + 256;
+constexpr int kPairSmem = kStages * kStageBytes + 8 * kWarpFloats * 4 + 1024;
 
 // One product: sums over `segs` pairs of operands a[s], b[s] in turn, or (z > 1)
 // z products with operands a[z] and the same b[0].
@@ -188,32 +190,18 @@ __device__ __forceinline__ void store16_staged(float *buf, void *out, int64_t ro
   store_rows(buf, out, row0 * N + ch, (int)max((int64_t)0, min((int64_t)32, M - row0)), N, valid, dtype);
 }
 
-// Sixteen channels' scales (or biases) from channel n on, `valid` of them there.
-__device__ __forceinline__ void channel16(const float *s, int64_t n, int valid, float (&v)[16]) {
-  if (valid >= 16) {
+// Int32 sums to fp32, times the token's scale and the channels' (sixteen floats in
+// shared memory).
+__device__ __forceinline__ void scale16(float (&v)[16], const float *c, float sa) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 q = __ldg(reinterpret_cast<const float4 *>(s + n) + i);
-      v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < valid ? __ldg(s + n + i) : 0.0f;
-  }
-}
-
-// Sums as fp32 (an int32 sum is rounded to fp32 here), scaled.
-template <bool I8>
-__device__ __forceinline__ void finish16(float (&v)[16], const float *s, int64_t n, int valid, float sa) {
-  if (!I8) return;
-  float c[16];
-  channel16(s, n, valid, c);
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const f2_t r = f2mul(f2mul(f2((float)__float_as_int(v[i]), (float)__float_as_int(v[i + 1])), f2(sa, sa)),
-                         f2(c[i], c[i + 1]));
+  for (int i = 0; i < 16; i += 4) {
+    const float4 q = *reinterpret_cast<const float4 *>(c + i);
+    const f2_t r = f2mul(f2mul(f2((float)__float_as_int(v[i]), (float)__float_as_int(v[i + 1])), f2(sa, sa)), f2(q.x, q.y));
+    const f2_t t = f2mul(f2mul(f2((float)__float_as_int(v[i + 2]), (float)__float_as_int(v[i + 3])), f2(sa, sa)), f2(q.z, q.w));
     v[i] = f2lo(r);
     v[i + 1] = f2hi(r);
+    v[i + 2] = f2lo(t);
+    v[i + 3] = f2hi(t);
   }
 }
 
@@ -340,8 +328,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp >= 2) {
     // ---- results: warp w reads the lanes of quarter w % 4, one half of the columns
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    float *stage = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)) + kStages * kStageBytes) +
-                   (warp - 2) * 32 * kStagePitch;
+    float *scales = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)) + kStages * kStageBytes) +
+                    (warp - 2) * kWarpFloats, *stage = scales + 256;
     int n_acc = 0;
     Tiles it;
     while (it.next(p, cluster)) {
@@ -354,6 +342,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int chunks = (DUAL ? 4 : 8) >> narrow, col0 = half * chunks * 16, up0 = narrow ? 64 : 128;
       const int64_t n0 = (int64_t)at.n * (DUAL ? 64 : 128) + col0;
       const float sa = I8 && in ? __ldg(p.e.a_scale + row) : 1.0f;
+      if (I8) {
+        // the columns' scales, while the products run: read chunk by chunk from L2 they took most of
+        // the epilogue (8-bit gated block 2048 x 2048 x 8192: 61.1 us so, 58.7 this way)
+        const float *second = DUAL ? p.e.s1 : p.e.bias;
+        __syncwarp();
+        for (int i = lane; i < 16 * chunks; i += 32) {
+          const bool there = n0 + i < j.N;
+          scales[i] = there ? __ldg(p.e.s0 + n0 + i) : 0.0f;
+          scales[128 + i] = there && second ? __ldg(second + n0 + i) : 0.0f;
+        }
+      }
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8 * buf, (n_acc >> 1) & 1, &stop))) break;
       tmem_fence_after_sync();
       const uint32_t t0 = tmem + buf * 256 + ((uint32_t)quarter << 21) + col0;
@@ -381,9 +380,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           continue;
         }
         const int64_t to = row * j.N + ch, row0 = row - lane;
-        finish16<I8>(g, p.e.s0, ch, valid, sa);
+        if (I8) scale16(g, scales + 16 * c, sa);
         if (DUAL) {
-          finish16<I8>(u, p.e.s1, ch, valid, sa);
+          if (I8) scale16(u, scales + 128 + 16 * c, sa);
           if (!I8 && p.e.gate) {
             if (valid == 16 && p.e.wide_save >= 16) {
               if (in) {
@@ -397,10 +396,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           gate(g, u, p.e.act);
         } else if (I8 && p.e.bias) {
-          float b[16];
-          channel16(p.e.bias, ch, valid, b);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) g[i] = __fadd_rn(g[i], b[i]);
+          for (int i = 0; i < 16; ++i) g[i] = __fadd_rn(g[i], scales[128 + 16 * c + i]);
         }
         if (valid == 16 && j.wide >= 16) {
           if (in) store16(j.out[at.z], to, p.e.dtype, g, j.wide);
