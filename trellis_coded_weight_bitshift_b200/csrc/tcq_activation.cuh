@@ -9,6 +9,21 @@ namespace tcq {
 // reciprocal is the right 0.
 __device__ __forceinline__ float logistic(float v) { return rcp(1.0f + ex2(-1.44269504f * v)); }
 
+// The normal distribution's density z and distribution function at v: for v >= 0
+// 1 - z (b1 t + .. + b5 t^5), t = 1 / (1 + 0.2316419 v), to within 7.5e-8
+// [Abramowitz and Stegun, Handbook of Mathematical Functions, 26.2.17].  Two
+// special-function instructions and nine others, where erfc takes about forty (8-bit
+// gated block 2048 x 2048 x 8192: 76.2 us with erfc, 61.4 so).
+__device__ __forceinline__ float normal_tail(float t, float z) {
+  return z * t *
+         fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.330274429f, -1.821255978f), 1.781477937f), -0.356563782f), 0.319381530f);
+}
+__device__ __forceinline__ void normal(float v, float &z, float &p) {
+  z = 0.39894228f * ex2(-0.72134752f * v * v);
+  const float q = normal_tail(rcp(fmaf(fabsf(v), 0.2316419f, 1.0f)), z);
+  p = v < 0.0f ? q : 1.0f - q;
+}
+
 // Value and slope of the activation at v.  The tanh form of gelu is
 // v * logistic(z), z = 2 sqrt(2/pi) (v + 0.044715 v^3).
 __device__ __forceinline__ void activation_slope(float v, int act, float &a, float &d) {
@@ -17,9 +32,10 @@ __device__ __forceinline__ void activation_slope(float v, int act, float &a, flo
     a = v * p;
     d = p + a * logistic(-v);
   } else if (act == TCQ_ACT_GELU) {
-    const float p = 0.5f * erfcf(-0.70710678f * v);
+    float z, p;
+    normal(v, z, p);
     a = v * p;
-    d = p + 0.39894228f * v * ex2(-0.72134752f * v * v);
+    d = p + v * z;
   } else if (act == TCQ_ACT_GELU_TANH) {
     const float vv = fminf(v * v, 1e30f);             // an infinite square would meet a zero below
     const float z = 1.59576912f * v * (1.0f + 0.044715f * vv);
@@ -48,8 +64,17 @@ __device__ __forceinline__ f2_t gated_pair(f2_t g, f2_t u) {
     return f2mul(f2mul(g, f2(rcp(f2lo(d)), rcp(f2hi(d)))), u);
   }
   if (ACT == TCQ_ACT_GELU) {
-    const f2_t p = f2(erfcf(-0.70710678f * f2lo(g)), erfcf(-0.70710678f * f2hi(g)));
-    return f2mul(f2mul(f2mul(g, f2(0.5f, 0.5f)), p), u);
+    const f2_t e = f2mul(f2mul(g, g), f2(-0.72134752f, -0.72134752f));
+    const f2_t z = f2mul(f2(ex2(f2lo(e)), ex2(f2hi(e))), f2(0.39894228f, 0.39894228f));
+    const f2_t d = f2fma(f2(fabsf(f2lo(g)), fabsf(f2hi(g))), f2(0.2316419f, 0.2316419f), f2(1.0f, 1.0f));
+    const f2_t t = f2(rcp(f2lo(d)), rcp(f2hi(d)));
+    f2_t q = f2fma(t, f2(1.330274429f, 1.330274429f), f2(-1.821255978f, -1.821255978f));
+    q = f2fma(t, q, f2(1.781477937f, 1.781477937f));
+    q = f2fma(t, q, f2(-0.356563782f, -0.356563782f));
+    q = f2fma(t, q, f2(0.319381530f, 0.319381530f));
+    q = f2mul(q, f2mul(t, z));
+    const float lo = f2lo(g) < 0.0f ? f2lo(q) : 1.0f - f2lo(q), hi = f2hi(g) < 0.0f ? f2hi(q) : 1.0f - f2hi(q);
+    return f2mul(f2mul(g, f2(lo, hi)), u);
   }
   return f2mul(f2(f2lo(g) < 0.0f ? 0.0f : f2lo(g), f2hi(g) < 0.0f ? 0.0f : f2hi(g)), u);
 }
