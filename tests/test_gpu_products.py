@@ -379,6 +379,13 @@ def test_autograd_takes_any_gradient_layout(tcq):
     _, g1, g2 = tcq.gated_ffn_backward(x, wg, wg, gate, up, grad)
     assert torch.equal(shared.grad, g1 + g2)
     assert not tcq.GatedFfn.apply(x, wg, wu).requires_grad
+    with torch.no_grad():
+        plain = tcq.GatedFfn.apply(xr, wr, wu)
+    assert not plain.requires_grad and torch.equal(plain, tcq.gated_ffn(x, wg, wu))
+    none = x[:0].clone().requires_grad_()
+    wr.grad = None
+    tcq.GatedFfn.apply(none, wr, wu).sum().backward()
+    assert none.grad.shape == (0, 24) and not bool(wr.grad.any())
     y = tcq.GatedFfn.apply(xr, wg, wu)
     (g,) = torch.autograd.grad(y.sum(), xr, create_graph=True)
     with pytest.raises(RuntimeError):

@@ -529,11 +529,19 @@ class GatedFfn(torch.autograd.Function):
     """h = GatedFfn.apply(x, w_gate, w_up, act): ``gated_ffn`` with its
     gradients.  It keeps the two projections in fp32 for the backward pass (8
     bytes a hidden value; rounded to 16 bits they would cost the gradients
-    more than the rounding of their own operands).  Twice differentiable it is
-    not: a second derivative raises."""
+    more than the rounding of their own operands); without gradients to
+    compute, or under ``torch.no_grad()``, it is ``gated_ffn``.  Twice
+    differentiable it is not: a second derivative raises."""
+
+    @classmethod
+    def apply(cls, x, w_gate, w_up, act=ACT_SILU):
+        # inside forward() the grad mode is always off, so it is asked here
+        if not torch.is_grad_enabled():
+            return gated_ffn(x, w_gate, w_up, act)
+        return super().apply(x, w_gate, w_up, act)
 
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, act=ACT_SILU):
+    def forward(ctx, x, w_gate, w_up, act):
         if not any(ctx.needs_input_grad[:3]):
             return gated_ffn(x, w_gate, w_up, act)
         sizes = _ffn_operands(x, w_gate, w_up)
