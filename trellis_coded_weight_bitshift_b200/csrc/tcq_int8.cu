@@ -10,9 +10,9 @@
 //   A row is read once: up to 4,096 bytes by one warp, up to 16,384 by a block,
 // into registers (16 bytes a load), its largest value is found, and it is
 // written; longer rows are read a second time.  Bound by HBM traffic, then by
-// issue: about five instructions a value (conversion, one fma, one subtraction,
-// one fma and a maximum for the check, byte packing; pairs where the hardware
-// has them).  Only where the check of eight values fails are they decided one by
+// issue: about five instructions a value (maximum, conversion, one fma, one
+// subtraction, one fma and a maximum for the check, byte packing; pairs where the
+// hardware has them).  Only where the check of eight values fails are they decided one by
 // one: a value lies that close to a border about once in 10^5.
 //
 // decode_int8: the 1MAD code is (bytesum - 510) / 147.8 [QTIP blog, "The
@@ -57,11 +57,17 @@ template <typename T, int N> struct Values {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-  // The largest |value|'s bits so far (16-bit types: one maximum for each half of the word).
+  // The largest |value|'s bits so far (16-bit types: one maximum for each half of the word; a NaN stays).
   __device__ __forceinline__ uint32_t top(uint32_t t) const {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i)
-      t = sizeof(T) == 4 ? max(t, w[i] & 0x7FFFFFFFu) : __vmaxu2(t, w[i] & 0x7FFF7FFFu);
+    for (int i = 0; i < kWords; ++i) {
+      if (sizeof(T) == 4)
+        t = max(t, w[i] & 0x7FFFFFFFu);
+      else if (std::is_same<T, __half>::value)
+        asm("{.reg .b32 a;\n abs.f16x2 a, %1;\n max.NaN.f16x2 %0, %0, a;}" : "+r"(t) : "r"(w[i]));
+      else
+        asm("{.reg .b32 a;\n abs.bf16x2 a, %1;\n max.NaN.bf16x2 %0, %0, a;}" : "+r"(t) : "r"(w[i]));
+    }
     return t;
   }
   __device__ __forceinline__ float get(int i) const {
@@ -80,12 +86,13 @@ __device__ __forceinline__ uint32_t top_as_f32(uint32_t t) {
   return std::is_same<T, __half>::value ? __float_as_uint(__half2float(__ushort_as_half(h))) : (uint32_t)h << 16;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void quantize_store(const Values<T, N> &v, float up, float scale, float inv, int8_t *q) {
+// UP: the values are multiplied by 2^64 first.
+template <typename T, int N, bool UP>
+__device__ __forceinline__ void quantize_store(const Values<T, N> &v, float scale, float inv, int8_t *q) {
   float x[N], worst = 0.0f;
   uint32_t u[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = v.get(i) * up;
+  for (int i = 0; i < N; ++i) x[i] = UP ? v.get(i) * 0x1p64f : v.get(i);
   if (N == 1) {
     q[0] = (int8_t)quantize_exactly(x[0], scale, inv);
     return;
@@ -95,7 +102,7 @@ __device__ __forceinline__ void quantize_store(const Values<T, N> &v, float up, 
     const f2_t xx = f2(x[2 * i], x[(2 * i + 1) % N]);
     const f2_t uu = f2fma(xx, f2(inv, inv), f2(kRound, kRound));
     const f2_t rr = f2fma(f2sub(f2(kRound, kRound), uu), f2(scale, scale), xx);
-    worst = fmaxf(worst, fmaxf(fabsf(f2lo(rr)), fabsf(f2hi(rr))));
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(worst) : "f"(f2lo(rr)), "f"(f2hi(rr)));
     u[2 * i] = __float_as_uint(f2lo(uu));
     u[(2 * i + 1) % N] = __float_as_uint(f2hi(uu));
   }
@@ -116,7 +123,7 @@ __device__ __forceinline__ void quantize_store(const Values<T, N> &v, float up, 
 // a thread kept in registers; what a longer row has beyond them is read twice.
 // Six blocks an SM keep enough loads in flight (4096 x 8192 bf16, GPU time: 17.8
 // us with the compiler's own 48 registers, 17.0 with six blocks, 23.9 with eight,
-// which spill).
+// which spill; 16.7 since the maxima take packed and three-operand instructions).
 template <typename T, int N, int TPR, int KEEP>
 __global__ void __launch_bounds__(256, TPR == 256 ? 6 : 4) quantize_rows_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
                                                             int8_t *__restrict__ q, float *__restrict__ scale) {
@@ -152,22 +159,27 @@ __global__ void __launch_bounds__(256, TPR == 256 ? 6 : 4) quantize_rows_kernel(
   const float amax = __uint_as_float(top), sc = __fdiv_rn(amax, 127.0f);
   const bool fine = top < 0x7F800000u;
   if (t == 0) scale[r] = fine ? sc : __uint_as_float(0x7FC00000u);
-  float up = amax < 0x1p-60f ? 0x1p64f : 1.0f;
-  const float by = sc * up;
+  const bool small = amax < 0x1p-60f;
+  const float by = small ? sc * 0x1p64f : sc;
   const float inv = fine && by > 0.0f ? 1.0f / by : 0.0f;
   if (!(inv > 0.0f)) {
     for (int64_t c = t; c < cols; c += TPR) out[c] = 0;
     return;
   }
+  const auto write = [&](auto up) {
+    constexpr bool kUp = decltype(up)::value;
 #pragma unroll
-  for (int i = 0; i < KEEP; ++i) {
-    const int64_t c = ((int64_t)i * TPR + t) * N;
-    if (c < cols) quantize_store<T, N>(v[i], up, by, inv, out + c);
-  }
-  for (int64_t c = ((int64_t)KEEP * TPR + t) * N; c < cols; c += (int64_t)TPR * N) {
-    w.load(row + c);
-    quantize_store<T, N>(w, up, by, inv, out + c);
-  }
+    for (int i = 0; i < KEEP; ++i) {
+      const int64_t c = ((int64_t)i * TPR + t) * N;
+      if (c < cols) quantize_store<T, N, kUp>(v[i], by, inv, out + c);
+    }
+    for (int64_t c = ((int64_t)KEEP * TPR + t) * N; c < cols; c += (int64_t)TPR * N) {
+      w.load(row + c);
+      quantize_store<T, N, kUp>(w, by, inv, out + c);
+    }
+  };
+  if (small) write(std::true_type());
+  else write(std::false_type());
 }
 
 // Two states' quarter numerators, each in the low byte of its half (the comment
