@@ -654,7 +654,6 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
-  if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
   cluster_sync();
 
   // each block finishes 128 / split of the channels, four a thread
@@ -677,6 +676,8 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
     const bool first = i < 192;
     finish4<I8, DUAL>(p.e, g, u, row, p.N, ch, valid, p.wide4, p.out, first ? &sa0 : nullptr, s00, s10);
   }
+  __syncwarp();
+  if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
   cluster_sync();                                        // no block leaves while its sums are read
   if (threadIdx.x == 0 && stop) atomicAdd(&g_gave_up, 1u);
 }
