@@ -1008,12 +1008,20 @@ tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
   if (cudaFuncSetAttribute(rows_kernel<I8, DUAL, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
       cudaSuccess)
     return TCQ_ERR_CUDA;
-  // Split the contraction while the blocks still fit the GPU at once and each keeps four steps of it.
-  // One int8 token, 8192 x 8192, in 1 / 2 / 4 / 8 parts: 21.4 / 15.6 / 15.5 / 20.7 us (the last in two
-  // waves); 2048 x 8192 with 64 tokens and one block an SM, 2 / 4 parts: 17.6 / 25.0.
-  const int64_t nt = tiles(p.N, 128), mt = tiles(p.M, NT), slots = (int64_t)sm_count() * Sh::kBlocksPerSm;
+  // Split the contraction while the clusters still fit the GPU at once (of 148 SMs, 132 hold clusters
+  // of four blocks and 120 clusters of eight) and each block keeps four steps of it, eight in a cluster
+  // of eight.  One int8 token, 8192 x 8192, in 1 / 2 / 4 / 8 parts: 21.4 / 15.6 / 15.5 / 20.7 us (the
+  // last in two waves); 16 tokens, 8192 -> 2048: 18.8 / 11.1 / 7.5 / 6.9; bf16 gated block of 16 tokens,
+  // 2048 -> 2048: 15.0 / 9.1 / 6.7 / 7.5 (four steps a block at eight parts), of 64 tokens, one block an
+  // SM: 18.1 / 11.8 / 9.2 / 19.6 (two waves).
+  const int64_t work = tiles(p.N, 128) * tiles(p.M, NT), sms = sm_count();
+  const auto fits = [&](int parts) {
+    const int64_t usable = parts == 8 ? sms * 13 / 16 : parts == 4 ? sms * 7 / 8 : sms;
+    return work * parts <= usable * Sh::kBlocksPerSm && p.kb >= (parts == 8 ? 64 : 4 * parts);
+  };
   int split = 1;
-  while (split < 8 && 2 * split * nt * mt <= slots && p.kb >= 8 * split) split *= 2;
+  while (split < 8 && fits(2 * split)) split *= 2;
+  const int64_t nt = tiles(p.N, 128), mt = tiles(p.M, NT);
   return launch(rows_kernel<I8, DUAL, NT>, dim3((unsigned)(nt * split), (unsigned)mt), 192, Sh::kSmem, split, s, p);
 }
 
