@@ -83,7 +83,8 @@ def _quantize_ref(x):
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (3, 2), (5, 31), (4, 32), (7, 255), (2, 256), (9, 1000), (3, 1024),
                                        (2, 1032), (5, 2047), (3, 4096), (2, 8191), (300, 8192), (2, 8200),
-                                       (1, 20000), (2, 33333)])
+                                       (1, 20000), (2, 33333),
+                                       (7, 2049), (5, 8185), (9, 4101), (40, 8190), (3, 2056), (2, 8193)])
 def test_quantize_equals_the_definition(tcq, dtype, rows, cols):
     x = (_randn(_gen(rows * 7 + cols), rows, cols) * 3).to(dtype)
     q, s = tcq.quantize_int8(x)
@@ -137,6 +138,22 @@ def test_quantize_special_rows(tcq):
     rq, rs = _quantize_ref(x[keep])
     assert torch.equal(q[keep], rq) and torch.equal(s[keep], rs)
     assert int(q[7, 0]) == -127 and float(s[0]) == 0.0
+
+
+@pytest.mark.parametrize("cols", [40, 2047, 2048, 2500, 5001, 8191, 9001])
+def test_quantize_special_rows_of_every_length(tcq, cols):
+    # the first and last places of rows that start anywhere; a row's neighbours do not reach it
+    x = _randn(_gen(cols), 9, cols)
+    x[1, 0], x[2, cols - 1], x[3, cols // 2] = float("inf"), float("nan"), float("-inf")
+    x[4] *= 2.0 ** -130
+    x[5] = 0
+    x[6, 0], x[7, cols - 1] = 900.0, -900.0
+    q, s = tcq.quantize_int8(x)
+    assert bool(torch.isnan(s[1:4]).all()) and not bool(q[1:4].any())
+    keep = [0, 4, 5, 6, 7, 8]
+    rq, rs = _quantize_ref(x[keep])
+    assert torch.equal(q[keep], rq) and torch.equal(s[keep], rs)
+    assert int(q[6, 0]) == 127 and int(q[7, cols - 1]) == -127
 
 
 # ------------------------------------------------------------ int8 decode
@@ -520,7 +537,7 @@ def _p(t):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 3, 5), (1, 136, 64), (17, 129, 33), (40, 77, 80), (70, 300, 128),
-                                   (257, 130, 45), (300, 264, 192)])
+                                   (257, 130, 45), (300, 264, 192), (5, 20, 3001), (3, 33, 8191)])
 def test_writes_stay_inside(tcq, M, N, K):
     lib, st = tcq.lib(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     x, wg, wu, grad = _ffn_inputs(1, M, N, K, F16)

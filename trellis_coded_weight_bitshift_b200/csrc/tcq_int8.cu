@@ -9,7 +9,8 @@
 // 1 / scale nor scale / 2 leaves the normal range.
 //   A row is read once: up to 4,096 bytes by one warp, up to 16,384 by a block,
 // into registers (16 bytes a load), its largest value is found, and it is
-// written; longer rows are read a second time.  Bound by HBM traffic, then by
+// written; longer rows are read a second time.  Rows that start anywhere go through
+// shared memory, whole aligned units on both sides.  Bound by HBM traffic, then by
 // issue: about five instructions a value (maximum, conversion, one fma, one
 // subtraction, one fma and a maximum for the check, byte packing; pairs where the
 // hardware has them).  Only where the check of eight values fails are they decided one by
@@ -182,6 +183,87 @@ __global__ void __launch_bounds__(256, TPR == 256 ? 6 : 4) quantize_rows_kernel(
   else write(std::false_type());
 }
 
+// The same for rows that start anywhere, a block a row of up to kAnyCols values:
+// the aligned 16-byte units that cover the row are read (what lies outside it
+// cleared), quantised to shared memory where a unit's place is aligned too, and
+// written in aligned units of the output, shifted as they are read back.  The two
+// units at the row's ends go by bytes.
+constexpr int kAnyCols = 8192;
+
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_rows_any_kernel(const T *__restrict__ x, int64_t rows, int cols,
+                                                                int8_t *__restrict__ q, float *__restrict__ scale) {
+  constexpr int N = 16 / (int)sizeof(T), KEEP = kAnyCols / (256 * N) + 1;
+  __shared__ __align__(16) int8_t row8[kAnyCols + 32];
+  __shared__ uint32_t part[8];
+  after_previous();
+  let_next_start();
+  const int t = threadIdx.x;
+  const T *row = x + (int64_t)blockIdx.x * cols, *end = x + rows * cols;
+  const int mis = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T)), units = (mis + cols + N - 1) / N;
+  const T *base = row - mis;
+  Values<T, N> v[KEEP];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int u = i * 256 + t;
+    v[i].zero();
+    if (u >= units) continue;
+    const T *at = base + (int64_t)u * N;
+    if (u > 0 && u < units - 1) {
+      v[i].load(at);
+    } else {                                             // the row's ends: its own values only
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int e = u * N + k - mis;
+        if (e >= 0 && e < cols) {
+          Values<T, 1> one;
+          one.load(at + k);
+          v[i].w[k * (int)sizeof(T) / 4] |= one.w[0] << (sizeof(T) == 2 ? 16 * (k & 1) : 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) top = v[i].top(top);
+  top = __reduce_max_sync(0xFFFFFFFFu, top_as_f32<T>(top));
+  if ((t & 31) == 0) part[t >> 5] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xFFFFFFFFu, part[t & 7]);
+  const float amax = __uint_as_float(top), sc = __fdiv_rn(amax, 127.0f);
+  const bool fine = top < 0x7F800000u, small = amax < 0x1p-60f;
+  if (t == 0) scale[blockIdx.x] = fine ? sc : __uint_as_float(0x7FC00000u);
+  const float by = small ? sc * 0x1p64f : sc;
+  const float inv = fine && by > 0.0f ? 1.0f / by : 0.0f;
+  int8_t *out = q + (int64_t)blockIdx.x * cols;
+  if (!(inv > 0.0f)) {
+    for (int c = t; c < cols; c += 256) out[c] = 0;
+    return;
+  }
+  const auto write = [&](auto up) {
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+      if (i * 256 + t < units)
+        quantize_store<T, N, decltype(up)::value>(v[i], by, inv, row8 + (i * 256 + t) * N);
+  };
+  if (small) write(std::true_type());
+  else write(std::false_type());
+  __syncthreads();
+  const int off = (int)(reinterpret_cast<uintptr_t>(out) & 15u);
+  for (int w = t; 16 * w < off + cols; w += 256) {
+    const int b = 16 * w - off, from = b + mis;
+    if (b >= 0 && b + 16 <= cols) {
+      const uint32_t *p = reinterpret_cast<const uint32_t *>(row8) + (from >> 2);
+      const uint32_t sh = 8 * (from & 3);
+      *reinterpret_cast<uint4 *>(out + b) =
+          make_uint4(__funnelshift_r(p[0], p[1], sh), __funnelshift_r(p[1], p[2], sh), __funnelshift_r(p[2], p[3], sh),
+                     __funnelshift_r(p[3], p[4], sh));
+    } else {
+      for (int k = max(0, -b); k < 16 && b + k < cols; ++k) out[b + k] = row8[from + k];
+    }
+  }
+}
+
 // Two states' quarter numerators, each in the low byte of its half (the comment
 // at the top).
 __device__ __forceinline__ f2_t quarter_codes(uint32_t state0, uint32_t state1) {
@@ -282,16 +364,20 @@ static tcq_status_t quantize_launch(const T *x, int64_t rows, int64_t cols, int8
   return launch(quantize_rows_kernel<T, N, TPR, KEEP>, dim3(blocks), 256, 0, 0, s, x, rows, cols, q, scale);
 }
 
-// Whole 16-byte loads where every row starts on such a boundary, else one value at a
-// time (4096 rows of bf16: 8192 values 17.7 us, 8191 values 41.2).  A warp a row
-// while the row fits its registers, else a block: 4096 rows of 512 values 2.4 us by
-// warps, 5.6 by blocks; 2048 values 5.1 and 7.3; 4096 values 13.8 and 11.0.  (Sixteen
-// rows of 2048: 2.2 and 1.4.)
+// Whole 16-byte loads where every row starts on such a boundary (4096 rows of bf16:
+// 8192 values 16.7 us).  Else the kernel for rows that start anywhere (8191 values
+// 25.0 us, one at a time 40.6; 4095: 17.8 and 22.0), but one value at a time for rows
+// of up to 2,048 (1023: 8.9 us, by that kernel 10.3) and those it does not hold.  A
+// warp a row while the row fits its registers, else a block: 4096 rows of 512 values
+// 2.4 us by warps, 5.6 by blocks; 2048 values 5.1 and 7.3; 4096 values 13.8 and 11.0.
+// (Sixteen rows of 2048: 2.2 and 1.4.)
 template <typename T>
 static tcq_status_t quantize_any(const T *x, int64_t rows, int64_t cols, int8_t *q, float *scale, cudaStream_t s) {
   constexpr int N = 16 / (int)sizeof(T);
   if (cols % N) {
     if (cols <= 256) return quantize_launch<T, 1, 32, 8>(x, rows, cols, q, scale, s);
+    if (cols > 2048 && cols <= kAnyCols)
+      return launch(quantize_rows_any_kernel<T>, dim3((unsigned)rows), 256, 0, 0, s, x, rows, (int)cols, q, scale);
     return quantize_launch<T, 1, 256, 8>(x, rows, cols, q, scale, s);
   }
   const int64_t loads = cols / N;
