@@ -265,7 +265,8 @@ def test_int8_gated_ffn(tcq, M, N, K, act, dtype):
 # after these: one token, a very long and a very wide matrix; few tiles and a long sum (split over
 # clusters) of the block, of grad_x and of the weights' gradients; half tiles in the last round
 FFN_SIZES = SIZES + [(1, 1000, 2048), (5, 8192, 64), (512, 384, 520), (3, 20, 100000), (70, 260, 4100),
-                     (140, 4100, 264), (129, 8200, 40), (5000, 200, 136), (700, 2500, 130), (2, 30000, 24)]
+                     (140, 4100, 264), (129, 8200, 40), (5000, 200, 136), (700, 2500, 130), (2, 30000, 24),
+                     (70000, 9, 24), (40000, 130, 7)]
 
 
 def _ffn_inputs(seed, M, N, K, dtype):
@@ -668,6 +669,40 @@ def test_results_repeat_bit_for_bit(tcq):
         assert torch.equal(again[0], h) and torch.equal(again[1], gate) and torch.equal(again[2], up)
         for a, b in zip(first, tcq.gated_ffn_backward(x, wg, wu, gate, up, grad)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,N,K", [(20, 72, 40), (300, 72, 40), (300, 77, 41), (130, 72, 9000)])
+def test_caller_owned_outputs_and_workspaces(tcq, M, N, K):
+    x, wg, wu, grad = _ffn_inputs(M, M, N, K, BF16)
+    h, gate, up = tcq.gated_ffn(x, wg, wu, save=True)
+    grads = tcq.gated_ffn_backward(x, wg, wu, gate, up, grad)
+    g = _gen(1)
+    a, sa, w, sw = _int8(g, M, K), _pos(g, M), _int8(g, N, K), _pos(g, N)
+    y, z = tcq.int8_matmul(a, sa, w, sw), tcq.int8_gated_ffn(a, sa, w, sw, w, sw, out_dtype=F32)
+    for extra in (0, 4096, -1):                      # exactly enough, more, too little (then one of its own)
+        def ws(need):
+            # filled with values that would show if a call relied on what it finds there
+            return torch.full((max(need + extra, 0),), 0x7F, dtype=torch.uint8, device="cuda")
+        out = torch.full((M, N), 9.0, dtype=BF16, device="cuda")
+        assert tcq.gated_ffn(x, wg, wu, out=out, workspace=ws(tcq.gated_ffn_workspace_size(M, N, K))) is out
+        assert torch.equal(out, h)
+        got = tcq.gated_ffn_backward(x, wg, wu, gate, up, grad,
+                                     workspace=ws(tcq.gated_ffn_backward_workspace_size(M, N, K)))
+        assert all(torch.equal(p, q) for p, q in zip(got, grads))
+        o16, o32 = torch.empty(M, N, dtype=F16, device="cuda"), torch.empty(M, N, device="cuda")
+        assert tcq.int8_matmul(a, sa, w, sw, out=o16, workspace=ws(tcq.int8_matmul_workspace_size(M, N, K))) is o16
+        assert torch.equal(o16, y)
+        tcq.int8_gated_ffn(a, sa, w, sw, w, sw, out_dtype=F32, out=o32,
+                           workspace=ws(tcq.int8_gated_ffn_workspace_size(M, N, K)))
+        assert torch.equal(o32, z)
+    if tcq.gated_ffn_backward_workspace_size(M, N, K):
+        odd = torch.empty(tcq.gated_ffn_backward_workspace_size(M, N, K) + 16, dtype=torch.uint8, device="cuda")[16:]
+        with pytest.raises(tcq.TcqError):
+            tcq.gated_ffn_backward(x, wg, wu, gate, up, grad, workspace=odd)
+    flat = torch.zeros(M * max(N, K), dtype=BF16, device="cuda")
+    onto = flat[:M * K].view(M, K)
+    with pytest.raises(tcq.TcqError):                # an output on top of an operand
+        tcq.gated_ffn(onto, wg, wu, out=flat[:M * N].view(M, N))
 
 
 def test_binding_refuses_misaligned_and_strided_operands(tcq):
