@@ -188,6 +188,14 @@ def test_decode_int8_tiles(tcq, L, layout, rows, cols):
     assert torch.equal(got, torch.round(k / 4).to(torch.int8))
 
 
+def test_decode_int8_refuses_shapes_that_are_not_the_tiles(tcq):
+    bits = torch.zeros(4, 16, dtype=torch.int32, device="cuda").view(torch.uint32)
+    for rows, cols, error in ((32, 48, tcq.TcqError), (30, 32, tcq.TcqError), (0, 0, tcq.TcqError),
+                              (-32, -32, ValueError)):
+        with pytest.raises(error):
+            tcq.decode_int8(bits, 16, 256, tcq.TAILBITING, tcq.OUT_TILE16, rows, cols)
+
+
 # ------------------------------------------------------------ int8 product
 
 SIZES = [(1, 1, 1), (1, 8, 16), (1, 256, 4096), (2, 17, 16), (3, 100, 33), (15, 129, 128), (16, 128, 256),

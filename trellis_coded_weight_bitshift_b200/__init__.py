@@ -29,6 +29,7 @@ Products on decoded weights:
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
@@ -103,6 +104,26 @@ def _ptr(t: "torch.Tensor | None") -> int:
 def _workspace(nbytes: int, device) -> torch.Tensor:
     # 256-byte aligned: the caching allocator hands out 512-byte aligned blocks
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+# torch.empty spends most of its 1.6 us on parsing its arguments; the entry point
+# that torch's own generated code allocates with takes 0.8 (a call of the products
+# below runs for 2 to 13 us on the GPU).  Both use the caching allocator.
+_empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
+                         "_empty_strided_cuda", None)
+
+
+def _empty(shape: tuple, dtype: torch.dtype) -> torch.Tensor:
+    """An uninitialised contiguous 1-D or 2-D tensor on the current device (the
+    one every operand was checked to be on)."""
+    if _empty_strided is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    return _empty_strided(shape, (1,) if len(shape) == 1 else (shape[1] or 1, 1), dtype)
+
+
+def _scratch(workspace: "torch.Tensor | None", need: int, like: torch.Tensor) -> torch.Tensor:
+    """As _use_workspace, for the products."""
+    return _empty((need or 256,), torch.uint8) if workspace is None else _use_workspace(workspace, need, like)
 
 
 def _use_workspace(workspace: "torch.Tensor | None", need: int, like: torch.Tensor) -> torch.Tensor:
@@ -367,11 +388,17 @@ def quantize_int8(x: torch.Tensor):
     if x.dim() != 2 or x.dtype not in _DTYPE:
         raise ValueError("x must be a 2-D float16, bfloat16 or float32 tensor")
     rows, cols = x.shape
-    q = torch.empty(rows, cols, dtype=torch.int8, device=x.device)
-    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    q, scale = _empty((rows, cols), torch.int8), _empty((rows,), torch.float32)
     check(lib().tcq_quantize_int8(_ptr(x), _DTYPE[x.dtype], rows, cols, _ptr(q), _ptr(scale),
                                   _stream()), "tcq_quantize_int8")
     return q, scale
+
+
+@lru_cache(maxsize=256)
+def _stream_shape(L: int, seq_len: int, layout: int):
+    """The trellis as the library takes it, and the words of a stream."""
+    tr = trellis(L, seq_len)
+    return tr, stream_words(L, seq_len, layout)
 
 
 def decode_int8(bits: torch.Tensor, L: int, seq_len: int = 256, layout: int = TAILBITING,
@@ -383,15 +410,16 @@ def decode_int8(bits: torch.Tensor, L: int, seq_len: int = 256, layout: int = TA
     if bits.dtype != torch.uint32 or bits.dim() != 2:
         raise ValueError("bits must be a 2-D uint32 tensor")
     n = bits.shape[0]
-    tr = trellis(L, seq_len)
-    words = int(lib().tcq_stream_words(ctypes.byref(tr), int(layout)))
+    tr, words = _stream_shape(int(L), int(seq_len), int(layout))
     if words == 0:
         raise TcqError(_abi.TCQ_ERR_UNSUPPORTED, "tcq_stream_words")
     if bits.shape[1] != words:
         raise ValueError(f"bits must have {words} words per sequence for this trellis and layout")
-    shape = (rows, cols) if out_layout == OUT_TILE16 else (n, seq_len)
+    shape = (int(rows), int(cols)) if out_layout == OUT_TILE16 else (n, int(seq_len))
+    if min(shape) < 0:
+        raise ValueError("rows and cols must not be negative")
     if out is None:
-        out = torch.empty(*shape, dtype=torch.int8, device=bits.device)
+        out = _empty(shape, torch.int8)
     else:
         _out(out, shape, torch.int8, bits)
     check(lib().tcq_decode_int8(ctypes.byref(tr), _ptr(bits), n, int(layout), int(out_layout),
@@ -421,8 +449,7 @@ def _int8_operands(a, a_scale, weights, bias=None):
 def _result(out, shape, dtype, like):
     if dtype not in _DTYPE:
         raise ValueError("the output type must be float16, bfloat16 or float32")
-    return (torch.empty(*shape, dtype=dtype, device=like.device) if out is None
-            else _out(out, shape, dtype, like))
+    return _empty(shape, dtype) if out is None else _out(out, shape, dtype, like)
 
 
 def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -434,7 +461,7 @@ def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     n_tok, n_out, n_in = _int8_operands(a, a_scale, (w, w_scale), bias)
     out = _result(out, (n_tok, n_out), out_dtype, a)
     need = int(lib().tcq_int8_matmul_workspace_size(n_tok, n_out, n_in))
-    ws = _use_workspace(workspace, need, a) if need else None
+    ws = _scratch(workspace, need, a) if need else None
     check(lib().tcq_int8_matmul(_ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(bias), n_tok,
                                 n_out, n_in, _ptr(out), _DTYPE[out_dtype], _ptr(ws),
                                 _nbytes(ws) if need else 0, _stream()), "tcq_int8_matmul")
@@ -451,7 +478,7 @@ def int8_gated_ffn(a: torch.Tensor, a_scale: torch.Tensor, w_gate: torch.Tensor,
     n_tok, n_out, n_in = _int8_operands(a, a_scale, (w_gate, w_gate_scale, w_up, w_up_scale))
     out = _result(out, (n_tok, n_out), out_dtype, a)
     need = int(lib().tcq_int8_gated_ffn_workspace_size(n_tok, n_out, n_in))
-    ws = _use_workspace(workspace, need, a) if need else None
+    ws = _scratch(workspace, need, a) if need else None
     check(lib().tcq_int8_gated_ffn(_ptr(a), _ptr(a_scale), _ptr(w_gate), _ptr(w_gate_scale),
                                    _ptr(w_up), _ptr(w_up_scale), n_tok, n_out, n_in, int(act),
                                    _ptr(out), _DTYPE[out_dtype], _ptr(ws),
@@ -474,7 +501,7 @@ def _ffn_operands(x, w_gate, w_up):
 def _launch_ffn(x, w_gate, w_up, act, sizes, out, gate, up, workspace):
     """gated_ffn on checked operands; gate and up: addresses, 0 for none."""
     need = int(lib().tcq_gated_ffn_workspace_size(*sizes))
-    ws = _use_workspace(workspace, need, x) if need else None
+    ws = _scratch(workspace, need, x) if need else None
     check(lib().tcq_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _DTYPE[x.dtype], *sizes, int(act),
                               _ptr(out), gate, up, _ptr(ws), _nbytes(ws) if need else 0, _stream()),
           "tcq_gated_ffn")
@@ -482,9 +509,9 @@ def _launch_ffn(x, w_gate, w_up, act, sizes, out, gate, up, workspace):
 
 def _launch_ffn_backward(x, w_gate, w_up, gate, up, grad_out, act, sizes, need, workspace):
     """gated_ffn_backward on checked operands; gate and up: addresses."""
-    grads = [torch.empty_like(t) if n else None for t, n in zip((x, w_gate, w_up), need)]
+    grads = [_empty(tuple(t.shape), t.dtype) if n else None for t, n in zip((x, w_gate, w_up), need)]
     size = int(lib().tcq_gated_ffn_backward_workspace_size(*sizes))
-    ws = _use_workspace(workspace, size, x)
+    ws = _scratch(workspace, size, x)
     check(lib().tcq_gated_ffn_backward(_ptr(x), _ptr(w_gate), _ptr(w_up), gate, up, _ptr(grad_out),
                                        _DTYPE[x.dtype], *sizes, int(act), _ptr(grads[0]),
                                        _ptr(grads[1]), _ptr(grads[2]), _ptr(ws), _nbytes(ws),
@@ -503,7 +530,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: in
     out = _result(out, sizes[:2], x.dtype, x)
     gate = up = None
     if save:
-        gate, up = (torch.empty(*sizes[:2], dtype=torch.float32, device=x.device) for _ in range(2))
+        gate, up = _empty(sizes[:2], torch.float32), _empty(sizes[:2], torch.float32)
     _launch_ffn(x, w_gate, w_up, act, sizes, out, _ptr(gate), _ptr(up), workspace)
     return (out, gate, up) if save else out
 
@@ -548,7 +575,7 @@ class GatedFfn(torch.autograd.Function):
         out = _result(None, sizes[:2], x.dtype, x)
         # both projections in one buffer, the second on a 16-byte boundary
         half = (sizes[0] * sizes[1] + 3) // 4 * 4
-        saved = torch.empty(2 * half, dtype=torch.float32, device=x.device)
+        saved = _empty((2 * half,), torch.float32)
         _launch_ffn(x, w_gate, w_up, act, sizes, out, _ptr(saved), _ptr(saved) + 4 * half, None)
         ctx.save_for_backward(x, w_gate, w_up, saved)
         ctx.act, ctx.sizes = act, sizes
