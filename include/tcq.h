@@ -315,7 +315,7 @@ TCQ_API tcq_status_t tcq_rht(const float *W, int64_t rows, int64_t cols, const f
  * a product is x W^T; n_tok counts tokens (rows of x).  n_tok = 0 is an empty
  * batch (weight gradients are then zero); a zero `rows`, `cols`, `n_out` or
  * `n_in` is an invalid argument.  Sizes are at most 2^30 - 1 each and the
- * product of any two of a matrix product's at most 2^42 (TCQ_ERR_UNSUPPORTED
+ * product of any two of a matrix product's at most 2^41 (TCQ_ERR_UNSUPPORTED
  * beyond), n_in of an int8 product at most 131,071 (its 32-bit sums cannot
  * overflow).  Any other size is taken; n_in a multiple of
  * 16 bytes (8 elements of 16 bits, 16 of int8) spares a copy of the operands

@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
   // each block finishes 128 / split of the channels, four a thread
   uint32_t peer[8];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) peer[r] = r < split ? map_to_rank(ring, r) : 0;
+  for (int r = 0; r < 8; ++r) peer[r] = map_to_rank(ring, r < split ? r : rank);
   for (int i = threadIdx.x; i < quads * cols; i += 192) {
     const int q = rank * quads + i % quads, c = i / quads;
     const int64_t ch = n0 + 4 * q, row = m0 + c;
@@ -667,11 +667,22 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
     if (valid <= 0) continue;
     const uint32_t off = 512 * c + 16 * q;
     float4 g = make_float4(0, 0, 0, 0), u = g;           // four zero bit patterns: int32 zeros too
+    // four parts' loads at a time: one after the other their latencies would add up
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      if (r >= split) break;
-      add4(g, ld_cluster4(peer[r] + off), I8);
-      if (DUAL) add4(u, ld_cluster4(peer[r] + off + 512 * NT), I8);
+    for (int r0 = 0; r0 < 8; r0 += 4) {
+      if (r0 >= split) break;
+      float4 a[4], b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[k] = ld_cluster4(peer[r0 + k] + off);          // past the last part: the block's own sums, not added
+        if (DUAL) b[k] = ld_cluster4(peer[r0 + k] + off + 512 * NT);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (r0 + k >= split) continue;
+        add4(g, a[k], I8);
+        if (DUAL) add4(u, b[k], I8);
+      }
     }
     const bool first = i < 192;
     finish4<I8, DUAL>(p.e, g, u, row, p.N, ch, valid, p.wide4, p.out, first ? &sa0 : nullptr, s00, s10);
