@@ -915,9 +915,10 @@ int clusters_of_gpu() { return std::max(1, sm_count() / 2); }
 // bytes: the number, of those that the clusters hold at once with eight steps or
 // more each, that takes the least time by what was measured: 0.26 us a step while
 // few clusters run, 3 us to join and the parts' sums twice through L2 at 6 TB/s.
-// Measured (us, whole / best split): int8 129 x 8192 x 1024 25.4 / 13.7 (eight
-// parts), 1024 tokens 26.7 / 19.6 (four); 129 x 8192 x 2048 26.2 / 16.1 (four);
-// not split 129 x 2048 x 2048 10.8 / 12.5 (two), 1024 x 8192 x 2048 27.4 / 27.7.
+// Measured (us, whole / best split): int8 512 x 8192 x 1024 25.8 / 16.9 (four
+// parts), 1024 tokens 26.7 / 19.6 (four); 512 x 8192 x 2048 26.8 / 19.9 (four); int8
+// gated block 129 x 8192 x 2048 26.4 / 19.5 (four); not split 512 x 2048 x 2048 11.1 /
+// 15.0 (two), 1024 x 8192 x 2048 27.4 / 27.7 (two).
 int parts_of(int64_t count, int64_t steps, double sums) {
   const int64_t most = std::min<int64_t>(clusters_of_gpu() / std::max<int64_t>(1, count), steps / 8);
   int best = 1;
@@ -1006,12 +1007,14 @@ tcq_status_t launch_pair(PairParams &p, int jobs, cudaStream_t s) {
   return st;
 }
 
-// Which kernel: up to 64 tokens (128 of a single product) rows_kernel.  Measured,
-// us, rows / pair: int8 8192 x 8192 at 64 tokens 17.1 / 24.0, 128 21.2 / 25.1, 256
-// 29.3 / 26.7; bf16 gated block 2048 -> 8192 at 64 17.6 / 19.3, 96 19.6 / 19.8, 128
-// 21.5 / 20.4; int8 gated block at 64 13.3 / 14.3, 96 15.6 / 14.6.
+// Which kernel: up to 64 tokens (256 of a single product) rows_kernel.  Measured,
+// us, rows / pair: int8 8192 x 8192 at 64 tokens 16.4 / 23.0, 128 19.7 / 27.7, 192
+// 27.5 / 30.4, 256 28.4 / 26.1, 384 43.2 / 33.9; 8192 -> 1024 at 256 11.6 / 14.0; 2048
+// x 2048 at 256 8.4 / 9.2; bf16 gated block 2048 -> 8192 at 64 17.3 / 19.7, 96 19.3 /
+// 20.2, 128 21.0 / 20.6, 1024 -> 2736 at 96 9.3 / 9.1; int8 gated block 2048 -> 8192
+// at 48 12.0 / 14.6, 64 13.3 / 13.0.
 template <bool DUAL>
-bool few_tokens(int64_t M) { return M <= (DUAL ? 64 : 128); }
+bool few_tokens(int64_t M) { return M <= (DUAL ? 64 : 256); }
 
 template <bool I8, bool DUAL, int NT>
 tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
