@@ -6,8 +6,8 @@
 // is complete and its writes are visible, and only then touches global memory.
 // let_next_start() allows the following kernel the same; it is called once every
 // block is past its start.  A kernel before it that never calls it simply
-// completes first.  Measured on 8-bit products of one token (8192 x 8192):
-// 15.5 us a pass without, 13.6 with.
+// completes first.  Measured on 8-bit products of one token (8192 x 8192): 15.5 us
+// a pass without, 14.5 with; on one quantised row 2.85 and 1.75.
 #pragma once
 
 #include <initializer_list>
