@@ -558,7 +558,9 @@ class GatedFfn(torch.autograd.Function):
     bytes a hidden value; rounded to 16 bits they would cost the gradients
     more than the rounding of their own operands); without gradients to
     compute, or under ``torch.no_grad()``, it is ``gated_ffn``.  Twice
-    differentiable it is not: a second derivative raises."""
+    differentiable it is not: a second derivative raises.  A step may be
+    captured into a CUDA graph once eager graphs of the same leaves are gone
+    (torch's own rule for captured backward passes)."""
 
     @classmethod
     def apply(cls, x, w_gate, w_up, act=ACT_SILU):
