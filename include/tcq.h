@@ -347,6 +347,8 @@ enum { TCQ_ACT_SILU = 0, TCQ_ACT_GELU = 1, TCQ_ACT_GELU_TANH = 2, TCQ_ACT_RELU =
  *   scale[m] = max_k |x[m][k]| / 127, rounded once to fp32,
  *   q[m][k]  = x[m][k] / scale[m] rounded to the nearest integer, ties to the
  *              even one (decided exactly, not on a rounded quotient).
+ * Where the scale is a subnormal of few digits (an fp32 row whose largest
+ * value is below 2.3e-41) x / scale can reach 127.5; q is then 127 in size.
  * A row of zeros (or one so small that its scale rounds to zero) gives scale
  * 0 and q 0; a row that holds an infinity or a NaN gives scale NaN and q 0, so
  * that a product with it shows the NaN.

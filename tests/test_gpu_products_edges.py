@@ -1,0 +1,45 @@
+"""Edges of the products on decoded weights: the smallest rows, the tails of the
+activations, early starts, reports of waits that ran out."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def tcq():
+    assert torch.cuda.is_available(), "GPU test"
+    from trellis_coded_weight_bitshift_b200.build import build
+    build()
+    import trellis_coded_weight_bitshift_b200 as t
+    return t
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, device="cuda", generator=g)
+
+
+# ------------------------------------------------------------ quantisation
+
+# every way a row is read: by warps and by blocks, in registers or twice, whole units or from anywhere, single values
+@pytest.mark.parametrize("cols", [3, 33, 40, 300, 1024, 2048, 2047, 2501, 5001, 5000, 9001])
+def test_quantize_rows_of_the_smallest_values(tcq, cols):
+    # values are whole numbers of 2^-149, the scale too: max / 127 to the nearest, ties to even; a scale of few
+    # units leaves quotients past 127, which are held there
+    tops = list(range(63, 202)) + [317, 318, 444, 5524, 5525, 8000, 16129, 16130, 20000, 40000]
+    g = torch.Generator().manual_seed(cols)
+    n = torch.stack([torch.randint(-t, t + 1, (cols,), generator=g) for t in tops]).double()
+    top = torch.tensor(tops).double()
+    n[:, 0], n[:, cols - 1] = top, -top
+    unit = torch.round(top / 127)
+    want = torch.where(unit[:, None] > 0, torch.round(n / unit.clamp(min=1)[:, None]), 0.0).clamp(-127, 127)
+    assert float((n.abs() / unit.clamp(min=1)[:, None]).max()) > 189          # the ranges hold what they are for
+    q, s = tcq.quantize_int8((n * 2.0 ** -149).float().cuda())
+    assert torch.equal(s.cpu().double(), unit * 2.0 ** -149)
+    assert torch.equal(q.cpu().double(), want)

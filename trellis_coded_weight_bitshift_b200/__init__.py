@@ -383,7 +383,8 @@ def quantize_int8(x: torch.Tensor):
     """Row-wise symmetric int8 quantisation of ``x`` [rows, cols] (fp16, bf16
     or fp32); returns (q int8 [rows, cols], scale fp32 [rows]) with x ~ q *
     scale: scale = max|row| / 127, q = x / scale rounded to nearest, ties to
-    even.  A zero row gives scale 0, a row with an infinity or NaN scale NaN."""
+    even, at most 127 in size.  A zero row gives scale 0, a row with an
+    infinity or NaN scale NaN."""
     _require_cuda(x)
     if x.dim() != 2 or x.dtype not in _DTYPE:
         raise ValueError("x must be a 2-D float16, bfloat16 or float32 tensor")

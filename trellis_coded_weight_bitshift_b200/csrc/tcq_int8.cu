@@ -6,7 +6,9 @@
 // multiple of half an ulp of scale, or finer with a smaller x, and at most
 // about half of scale), and |r| against scale / 2 says whether q0 stays.
 // Rows below 2^-60 are first multiplied by 2^64 (exact), so that neither
-// 1 / scale nor scale / 2 leaves the normal range.
+// 1 / scale nor scale / 2 leaves the normal range.  Among them are rows whose scale is a
+// subnormal of fewer than 127 units of 2^-149: rounding max / 127 to so few digits can leave
+// x / scale at 127.5 and more (190 units: scale 1), which is then +-127.
 //   A row is read once: up to 4,096 bytes by one warp, up to 16,384 by a block,
 // into registers (16 bytes a load), its largest value is found, and it is
 // written; longer rows are read a second time.  Rows that start anywhere go through
@@ -39,6 +41,11 @@ __device__ __forceinline__ uint32_t quantize_exactly(float x, float scale, float
   const float r = __fmaf_rn(-__fsub_rn(u, kRound), scale, x), half = 0.5f * scale;
   if (fabsf(r) > half || (fabsf(r) == half && (__float_as_uint(u) & 1u))) u = __fadd_rn(u, copysignf(1.0f, r));
   return __float_as_uint(u);
+}
+
+// The same bits with the integer held to -127 .. 127.
+__device__ __forceinline__ uint32_t within_127(uint32_t u) {
+  return __float_as_uint(fminf(fmaxf(__uint_as_float(u), kRound - 127.0f), kRound + 127.0f));
 }
 
 // N values (1, 4 or 8) of one thread, as they are loaded: raw words of type T.
@@ -87,7 +94,8 @@ __device__ __forceinline__ uint32_t top_as_f32(uint32_t t) {
   return std::is_same<T, __half>::value ? __float_as_uint(__half2float(__ushort_as_half(h))) : (uint32_t)h << 16;
 }
 
-// UP: the values are multiplied by 2^64 first.
+// UP: the values are multiplied by 2^64 first, and the results held to +-127 (other rows'
+// quotients are within 127 (1 + 2^-23)).
 template <typename T, int N, bool UP>
 __device__ __forceinline__ void quantize_store(const Values<T, N> &v, float scale, float inv, int8_t *q) {
   float x[N], worst = 0.0f;
@@ -95,7 +103,8 @@ __device__ __forceinline__ void quantize_store(const Values<T, N> &v, float scal
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = UP ? v.get(i) * 0x1p64f : v.get(i);
   if (N == 1) {
-    q[0] = (int8_t)quantize_exactly(x[0], scale, inv);
+    u[0] = quantize_exactly(x[0], scale, inv);
+    q[0] = (int8_t)(UP ? within_127(u[0]) : u[0]);
     return;
   }
 #pragma unroll
@@ -110,6 +119,10 @@ __device__ __forceinline__ void quantize_store(const Values<T, N> &v, float scal
   if (worst >= 0.5f * scale) {
 #pragma unroll
     for (int i = 0; i < N; ++i) u[i] = quantize_exactly(x[i], scale, inv);
+  }
+  if (UP) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = within_127(u[i]);
   }
   uint32_t b[(N + 3) / 4];
 #pragma unroll
