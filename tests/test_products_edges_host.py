@@ -1,0 +1,35 @@
+"""Products on decoded weights, what can be shown without a GPU: how their
+sources load, what the binding does at its edges."""
+import glob
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "trellis_coded_weight_bitshift_b200", "csrc")
+
+
+def _code(path):
+    """A source without its comments."""
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", open(path).read(), flags=re.S)
+
+
+def test_kernels_that_start_early_use_no_read_only_loads():
+    # a kernel launched by tcq_launch.cuh runs while its predecessor still writes: no load of its may be one that
+    # the compiler takes for constant (and moves above the wait), in its source or in a header that it includes
+    early = [p for p in glob.glob(os.path.join(CSRC, "*.cu")) if '"tcq_launch.cuh"' in open(p).read()]
+    assert len(early) >= 2
+    headers = [os.path.join(CSRC, h) for h in ("tcq_launch.cuh", "tcq_tensor.cuh", "tcq_activation.cuh")]
+    for path in early + headers:
+        code = _code(path)
+        found = re.findall(r"__ldg\b|ld\.global\.nc|const\s+\w+\s*\*\s*(?:const\s+)?__restrict__\s*\w+", code)
+        assert not found, (path, found)
+
+
+def test_every_kernel_waits_before_it_lets_the_next_start():
+    # the next kernel may start once all blocks have called let_next_start: after their own wait, not before
+    for path in glob.glob(os.path.join(CSRC, "*.cu")):
+        if '"tcq_launch.cuh"' not in open(path).read():
+            continue
+        for body in re.split(r"\n__global__", _code(path))[1:]:
+            body = body.split("\n}\n")[0]
+            assert 0 <= body.find("after_previous()") < body.find("let_next_start()"), (path, body[:120])

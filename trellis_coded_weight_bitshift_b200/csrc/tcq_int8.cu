@@ -54,10 +54,9 @@ template <typename T, int N> struct Values {
   uint32_t w[kWords];
   __device__ __forceinline__ void load(const T *p) {
     if (N == 1) {
-      w[0] = sizeof(T) == 4 ? __ldg(reinterpret_cast<const uint32_t *>(p))
-                            : __ldg(reinterpret_cast<const unsigned short *>(p));
+      w[0] = sizeof(T) == 4 ? ld_u32(p) : (uint32_t)ld_u16(p);
     } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+      const uint4 v = ld_u32x4(p);
       w[0] = v.x; w[1 % kWords] = v.y; w[2 % kWords] = v.z; w[3 % kWords] = v.w;
     }
   }
@@ -139,7 +138,7 @@ __device__ __forceinline__ void quantize_store(const Values<T, N> &v, float scal
 // us with the compiler's own 48 registers, 17.0 with six blocks, 23.9 with eight,
 // which spill; 16.7 since the maxima take packed and three-operand instructions).
 template <typename T, int N, int TPR, int KEEP>
-__global__ void __launch_bounds__(256, TPR == 256 ? 6 : 4) quantize_rows_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
+__global__ void __launch_bounds__(256, TPR == 256 ? 6 : 4) quantize_rows_kernel(const T *x, int64_t rows, int64_t cols,
                                                             int8_t *__restrict__ q, float *__restrict__ scale) {
   __shared__ uint32_t part[8];
   after_previous();
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(256, TPR == 256 ? 6 : 4) quantize_rows_kernel(
 constexpr int kAnyCols = 8192;
 
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_rows_any_kernel(const T *__restrict__ x, int64_t rows, int cols,
+__global__ void __launch_bounds__(256) quantize_rows_any_kernel(const T *x, int64_t rows, int cols,
                                                                 int8_t *__restrict__ q, float *__restrict__ scale) {
   constexpr int N = 16 / (int)sizeof(T), KEEP = kAnyCols / (256 * N) + 1;
   __shared__ __align__(16) int8_t row8[kAnyCols + 32];
@@ -312,7 +311,7 @@ __device__ __forceinline__ uint4 decode16(uint32_t hi, uint32_t lo) {
 // One thread per 16 x 16 tile: its stream in registers, a row of it in one
 // 16-byte store; a warp's stores cover 512 neighbouring bytes.
 template <int L, int LAYOUT>
-__global__ void __launch_bounds__(128) decode_int8_tiles_kernel(const uint32_t *__restrict__ bits, int64_t n_seq,
+__global__ void __launch_bounds__(128) decode_int8_tiles_kernel(const uint32_t *bits, int64_t n_seq,
                                                                 int tiles_c, int wps, int8_t *__restrict__ out) {
   after_previous();
   let_next_start();
@@ -323,13 +322,13 @@ __global__ void __launch_bounds__(128) decode_int8_tiles_kernel(const uint32_t *
   if (LAYOUT == TCQ_TAILBITING) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+      const uint4 v = ld_u32x4(src + 4 * i);
       w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
     }
     w[16] = w[0];
   } else {
 #pragma unroll
-    for (int i = 0; i < 17; ++i) w[i] = __ldg(src + i);
+    for (int i = 0; i < 17; ++i) w[i] = ld_u32(src + i);
   }
   const int64_t tr = seq / tiles_c, tc = seq - tr * tiles_c, cols = (int64_t)tiles_c * 16;
   int8_t *dst = out + tr * 16 * cols + tc * 16;
@@ -340,7 +339,7 @@ __global__ void __launch_bounds__(128) decode_int8_tiles_kernel(const uint32_t *
 // One thread per word of the stream, sixteen weights in sequence order (T a
 // multiple of 16: one 16-byte store), the last word's fewer.
 template <int L>
-__global__ void __launch_bounds__(256) decode_int8_seq_kernel(const uint32_t *__restrict__ bits, int64_t n_items,
+__global__ void __launch_bounds__(256) decode_int8_seq_kernel(const uint32_t *bits, int64_t n_items,
                                                               int per_seq, int T, int layout, int wps,
                                                               int8_t *__restrict__ out) {
   after_previous();
@@ -349,8 +348,8 @@ __global__ void __launch_bounds__(256) decode_int8_seq_kernel(const uint32_t *__
     const int64_t seq = g / per_seq;
     const int i = (int)(g - seq * per_seq);
     const uint32_t *src = bits + seq * wps;
-    const uint32_t lo = i + 1 < wps ? __ldg(src + i + 1) : layout == TCQ_TAILBITING ? __ldg(src) : 0u;
-    const uint4 v = decode16<L>(__ldg(src + i), lo);
+    const uint32_t lo = i + 1 < wps ? ld_u32(src + i + 1) : layout == TCQ_TAILBITING ? ld_u32(src) : 0u;
+    const uint4 v = decode16<L>(ld_u32(src + i), lo);
     int8_t *dst = out + seq * T + 16 * i;
     if (T % 16 == 0) {
       *reinterpret_cast<uint4 *>(dst) = v;

@@ -6,7 +6,15 @@
 // is complete and its writes are visible, and only then touches global memory.
 // let_next_start() allows the following kernel the same; it is called once every
 // block is past its start.  A kernel before it that never calls it simply
-// completes first.  Measured on 8-bit products of one token (8192 x 8192): 15.5 us
+// completes first.
+//
+// Such a kernel lives while its predecessor still writes, so nothing that an earlier
+// kernel may have written is constant for its lifetime: the read-only path (__ldg, or
+// const __restrict__ pointers, which become it) is not allowed to it, and the compiler may
+// move such loads above the wait.  Operands are read by the ld_* loads below, ordinary
+// loads that stay behind after_previous().
+//
+// Measured on 8-bit products of one token (8192 x 8192): 15.5 us
 // a pass without, 14.5 with; on one quantised row 2.85 and 1.75.
 #pragma once
 
@@ -19,6 +27,37 @@ namespace tcq {
 
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 ld_u32x4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_f32x4(const float *p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u32(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_f32(const float *p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_u16(const void *p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u8(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 
 }  // namespace tcq
 

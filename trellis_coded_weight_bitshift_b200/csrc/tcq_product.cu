@@ -347,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const bool in = row < j.M;
       const int chunks = (DUAL ? 4 : 8) >> narrow, col0 = half * chunks * 16, up0 = narrow ? 64 : 128;
       const int64_t n0 = (int64_t)at.n * (DUAL ? 64 : 128) + col0;
-      const float sa = I8 && in ? __ldg(p.e.a_scale + row) : 1.0f;
+      const float sa = I8 && in ? ld_f32(p.e.a_scale + row) : 1.0f;
       if (I8) {
         // the columns' scales, while the products run: read chunk by chunk from L2 they took most of
         // the epilogue (8-bit gated block 2048 x 2048 x 8192: 61.1 us so, 58.7 this way)
@@ -355,8 +355,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         for (int i = lane; i < 16 * chunks; i += 32) {
           const bool there = n0 + i < j.N;
-          scales[i] = there ? __ldg(p.e.s0 + n0 + i) : 0.0f;
-          scales[128 + i] = there && second ? __ldg(second + n0 + i) : 0.0f;
+          scales[i] = there ? ld_f32(p.e.s0 + n0 + i) : 0.0f;
+          scales[128 + i] = there && second ? ld_f32(second + n0 + i) : 0.0f;
         }
       }
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8 * buf, (n_acc >> 1) & 1, &stop))) break;
@@ -461,13 +461,13 @@ __device__ __forceinline__ void finish4(const Epilogue &e, const float4 &g, cons
   float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
   const int64_t at = row * N + ch;
   if (I8) {
-    const float s = sa ? *sa : __ldg(e.a_scale + row);
+    const float s = sa ? *sa : ld_f32(e.a_scale + row);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (k >= valid) continue;
-      gv[k] = (float)__float_as_int(gv[k]) * s * (sa ? c0[k] : __ldg(e.s0 + ch + k));
-      if (DUAL) uv[k] = (float)__float_as_int(uv[k]) * s * (sa ? c1[k] : __ldg(e.s1 + ch + k));
-      else if (e.bias) gv[k] = __fadd_rn(gv[k], sa ? c1[k] : __ldg(e.bias + ch + k));
+      gv[k] = (float)__float_as_int(gv[k]) * s * (sa ? c0[k] : ld_f32(e.s0 + ch + k));
+      if (DUAL) uv[k] = (float)__float_as_int(uv[k]) * s * (sa ? c1[k] : ld_f32(e.s1 + ch + k));
+      else if (e.bias) gv[k] = __fadd_rn(gv[k], sa ? c1[k] : ld_f32(e.bias + ch + k));
     }
   }
   if (DUAL) {
@@ -525,8 +525,8 @@ __global__ void __launch_bounds__(256) join_kernel(const Join p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const bool there = s + k < p.split;
-        a[k] = there ? __ldg(reinterpret_cast<const float4 *>(at + (s + k) * part)) : make_float4(0, 0, 0, 0);
-        if (DUAL) b[k] = there ? __ldg(reinterpret_cast<const float4 *>(at + (s + k) * part + plane)) : make_float4(0, 0, 0, 0);
+        a[k] = there ? ld_f32x4(at + (s + k) * part) : make_float4(0, 0, 0, 0);
+        if (DUAL) b[k] = there ? ld_f32x4(at + (s + k) * part + plane) : make_float4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -591,13 +591,13 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
   float sa0 = 0.0f, s00[4] = {}, s10[4] = {};
   if (I8 && threadIdx.x < quads * cols) {
     const int64_t ch = n0 + 4 * (rank * quads + (int)threadIdx.x % quads);
-    sa0 = __ldg(p.e.a_scale + m0 + threadIdx.x / quads);
+    sa0 = ld_f32(p.e.a_scale + m0 + threadIdx.x / quads);
     const float *second = DUAL ? p.e.s1 : p.e.bias;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (ch + k >= p.N) continue;
-      s00[k] = __ldg(p.e.s0 + ch + k);
-      if (second) s10[k] = __ldg(second + ch + k);
+      s00[k] = ld_f32(p.e.s0 + ch + k);
+      if (second) s10[k] = ld_f32(second + ch + k);
     }
   }
   tmem_fence_before_sync();
@@ -723,7 +723,7 @@ struct PitchCopies {
 __device__ __noinline__ uint4 unit_before(const uint8_t *a, const uint8_t *end) {
   uint32_t w[4] = {};
   for (int q = 0; q < 16; ++q)
-    if (a + q < end) w[q >> 2] |= (uint32_t)a[q] << (8 * (q & 3));
+    if (a + q < end) w[q >> 2] |= ld_u8(a + q) << (8 * (q & 3));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -745,9 +745,9 @@ __global__ void __launch_bounds__(256) pitch_rows_kernel(const PitchCopies p) {
       const uint8_t *a = base + 16 * (int64_t)c;
       const int left = (int)min((int64_t)16, m.bytes - 16 * (int64_t)c);
       uint4 u, v = make_uint4(0, 0, 0, 0);
-      u = safe || a + 16 <= end ? __ldg(reinterpret_cast<const uint4 *>(a)) : unit_before(a, end);
+      u = safe || a + 16 <= end ? ld_u32x4(a) : unit_before(a, end);
       if (left + (int)mis > 16)
-        v = safe || a + 32 <= end ? __ldg(reinterpret_cast<const uint4 *>(a + 16)) : unit_before(a + 16, end);
+        v = safe || a + 32 <= end ? ld_u32x4(a + 16) : unit_before(a + 16, end);
       uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
       if (mis & 8u) {
 #pragma unroll
@@ -783,8 +783,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float
 // values a thread where rows start on 16-byte boundaries (N = 8), else one.  Bound by
 // HBM: 4096 x 8192 bf16, 470 MB in 65 us (7.2 TB/s).
 template <typename T, int N>
-__global__ void __launch_bounds__(256) gate_grad_kernel(const T *__restrict__ grad, const float *__restrict__ gate,
-                                                        const float *__restrict__ up, int64_t rows, int64_t cols,
+__global__ void __launch_bounds__(256) gate_grad_kernel(const T *grad, const float *gate,
+                                                        const float *up, int64_t rows, int64_t cols,
                                                         int64_t pitch, int act, T *__restrict__ dg,
                                                         T *__restrict__ du) {
   after_previous();
@@ -795,16 +795,15 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const T *__restrict__ gr
     const int64_t at = r * cols + c, to = r * pitch + c;
     if (N == 1) {
       float a, d;
-      activation_slope(__ldg(gate + at), act, a, d);
-      const float h = widen<T>(grad[at]);
-      dg[to] = narrow<T>(h * __ldg(up + at) * d);
+      activation_slope(ld_f32(gate + at), act, a, d);
+      const uint16_t bits = ld_u16(grad + at);
+      const float h = widen<T>(*reinterpret_cast<const T *>(&bits));
+      dg[to] = narrow<T>(h * ld_f32(up + at) * d);
       du[to] = narrow<T>(h * a);
     } else {
-      const uint4 hv = __ldg(reinterpret_cast<const uint4 *>(grad + at));
-      const float4 g0 = __ldg(reinterpret_cast<const float4 *>(gate + at)),
-                   g1 = __ldg(reinterpret_cast<const float4 *>(gate + at) + 1),
-                   u0 = __ldg(reinterpret_cast<const float4 *>(up + at)),
-                   u1 = __ldg(reinterpret_cast<const float4 *>(up + at) + 1);
+      const uint4 hv = ld_u32x4(grad + at);
+      const float4 g0 = ld_f32x4(gate + at), g1 = ld_f32x4(gate + at + 4), u0 = ld_f32x4(up + at),
+                   u1 = ld_f32x4(up + at + 4);
       const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
       const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
       const T *h = reinterpret_cast<const T *>(&hv);
