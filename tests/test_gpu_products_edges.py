@@ -43,3 +43,18 @@ def test_quantize_rows_of_the_smallest_values(tcq, cols):
     q, s = tcq.quantize_int8((n * 2.0 ** -149).float().cuda())
     assert torch.equal(s.cpu().double(), unit * 2.0 ** -149)
     assert torch.equal(q.cpu().double(), want)
+
+
+# ------------------------------------------------------------ waits that run out
+
+def test_the_count_of_waits_covers_every_stream(tcq):
+    # torch's side streams do not block the default one: the count has to wait for them itself
+    side = torch.cuda.Stream()
+    done = torch.cuda.Event()
+    tcq.products_gave_up()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)                   # about 0.1 s
+        done.record()
+    assert not done.query()
+    assert tcq.products_gave_up() == 0
+    assert done.query()

@@ -1054,6 +1054,8 @@ tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
 
 extern "C" tcq_status_t tcq_products_gave_up(unsigned int *count) {
   if (!count) return TCQ_ERR_INVALID_ARG;
+  // the copy alone would not wait for non-blocking streams
+  if (cudaDeviceSynchronize() != cudaSuccess) return TCQ_ERR_CUDA;
   return cudaMemcpyFromSymbol(count, g_gave_up, sizeof(unsigned)) == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA;
 }
 
