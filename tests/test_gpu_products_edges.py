@@ -1,5 +1,7 @@
 """Edges of the products on decoded weights: the smallest rows, the tails of the
 activations, early starts, reports of waits that ran out."""
+import ctypes
+
 import pytest
 import torch
 
@@ -58,3 +60,15 @@ def test_the_count_of_waits_covers_every_stream(tcq):
     assert not done.query()
     assert tcq.products_gave_up() == 0
     assert done.query()
+
+
+def test_a_wait_that_nothing_meets_ends(tcq, tmp_path):
+    from native import compiled
+    out = torch.zeros(8, dtype=torch.int64, device="cuda")
+    lib = compiled("waits", tmp_path)
+    assert lib.wait_runs_out(ctypes.c_ulonglong(20_000_000), ctypes.c_void_p(out.data_ptr())) == 0
+    met0, t0, met1, t1, met2, t2, stop, _ = out.tolist()
+    # the limit ends the first wait (looked at every 32 tries, of a millisecond each at most), its flag the second;
+    # one that is met is met
+    assert (met0, met1, met2, stop) == (0, 0, 1, 1)
+    assert 20e6 <= t0 < 150e6 and t1 < 300e6 and t2 < 5e6

@@ -1,5 +1,6 @@
 """Products on decoded weights, what can be shown without a GPU: how their
 sources load, what the binding does at its edges."""
+import ctypes
 import glob
 import os
 import re
@@ -33,3 +34,20 @@ def test_every_kernel_waits_before_it_lets_the_next_start():
         for body in re.split(r"\n__global__", _code(path))[1:]:
             body = body.split("\n}\n")[0]
             assert 0 <= body.find("after_previous()") < body.find("let_next_start()"), (path, body[:120])
+
+
+def test_time_in_which_a_kernel_did_not_run_is_not_waited(tmp_path):
+    # a wait's clock goes on while another process has the GPU: two looks seconds apart are no wait of seconds
+    from native import compiled
+    lib = compiled("waits", tmp_path)
+
+    def over(at, limit):
+        got = (ctypes.c_int * len(at))()
+        lib.waited((ctypes.c_ulonglong * len(at))(*at), len(at), ctypes.c_ulonglong(limit), got)
+        return list(got)[1:]
+    ms, s = 10 ** 6, 10 ** 9
+    looks = [i * 32 * ms for i in range(80)]                       # a look every 32 ms
+    assert over(looks, 2 * s) == [i * 32 * ms > 2 * s for i in range(1, 80)]
+    held = [0, 32 * ms, 10 * s, 10 * s + 32 * ms, 10 * s + 64 * ms]
+    assert not any(over(held, 2 * s))
+    assert over([i * 60 * s for i in range(43)], 2 * s) == [False] * 40 + [True, True]      # and it does end

@@ -7,7 +7,7 @@
 // ("MN-major": 64 of its 16-bit columns wide, 64 deep) is one 8 KB block for
 // each 64 columns, 8 groups of 1,024 bytes along the contraction.
 //
-// Every wait gives up after two seconds: it raises the block's `stop` flag, at
+// Every wait gives up after two seconds of polling: it raises the block's `stop` flag, at
 // which the block's other waits end too, the copies in flight are waited for,
 // tensor memory is freed and the kernel returns; the library-wide counter
 // g_gave_up then says so.
@@ -56,16 +56,31 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned long long kWaitNs = 2000000000ull, kGapNs = 50000000ull;
+
+// Time spent polling.  The clock runs on while another process has the GPU, so the time
+// between two looks counts as kGapNs at most (32 tries of a millisecond take less): a
+// kernel held up for seconds does not find its waits over when it goes on.
+struct Waited {
+  unsigned long long last, sum;
+  __host__ __device__ explicit Waited(unsigned long long now) : last(now), sum(0) {}
+  __host__ __device__ bool over(unsigned long long now, unsigned long long limit) {
+    const unsigned long long gap = now - last;
+    sum += gap < kGapNs ? gap : kGapNs;
+    last = now;
+    return sum > limit;
+  }
+};
 
 // True once the phase of `parity` is over; false when `stop` is up or the time
 // is (then `stop` goes up).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t *stop) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t *stop,
+                                          unsigned long long limit = kWaitNs) {
   if (mbar_try(bar, parity)) return true;
-  const unsigned long long t0 = now_ns();
+  Waited waited(now_ns());
   for (uint32_t i = 1; i < (1u << 30); ++i) {
     if (mbar_try(bar, parity)) return true;
-    if ((i & 31u) == 0 && (*stop || now_ns() - t0 > kWaitNs)) break;
+    if ((i & 31u) == 0 && (*stop || waited.over(now_ns(), limit))) break;
   }
   *stop = 1u;
   return false;
