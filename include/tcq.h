@@ -331,11 +331,11 @@ TCQ_API tcq_status_t tcq_rht(const float *W, int64_t rows, int64_t cols, const f
  * ------------------------------------------------------------------------ */
 
 /* How often a product's kernel gave up waiting for its own loads or products
- * (two seconds of polling
- * each; time in which the kernel did not run counts little) on the current device since the library was loaded: 0
- * unless something is wrong; the outputs of such a call are unspecified.
- * Waits for the whole device, every stream of it; not allowed while a stream
- * is captured. */
+ * (after two seconds of polling; time in which the kernel did not run hardly
+ * counts) on the current device since the library was loaded: 0 unless
+ * something is wrong; the outputs of such a call are unspecified.  Waits for
+ * the whole device, every stream of it; not allowed while a stream is
+ * captured. */
 TCQ_API tcq_status_t tcq_products_gave_up(unsigned int *count);
 
 enum { TCQ_F16 = 0, TCQ_BF16 = 1, TCQ_F32 = 2 };

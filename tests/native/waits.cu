@@ -39,3 +39,18 @@ EXPORT int wait_runs_out(unsigned long long limit, unsigned long long *out) {
   wait_kernel<<<1, 96>>>(limit, out);
   return (int)cudaDeviceSynchronize();
 }
+
+// A barrier that nothing arrives at, waited for as an aborted block does before it leaves.
+__global__ void drain_kernel(unsigned long long *out) {
+  __shared__ __align__(8) uint64_t bar;
+  mbar_init(smem_u32(&bar), 1);
+  mbar_init_fence();
+  const unsigned long long t0 = now_ns();
+  mbar_drain(smem_u32(&bar), 0);
+  out[0] = now_ns() - t0;
+}
+
+EXPORT int drain_ends(unsigned long long *out) {
+  drain_kernel<<<1, 1>>>(out);
+  return (int)cudaDeviceSynchronize();
+}

@@ -72,3 +72,5 @@ def test_a_wait_that_nothing_meets_ends(tcq, tmp_path):
     # one that is met is met
     assert (met0, met1, met2, stop) == (0, 0, 1, 1)
     assert 20e6 <= t0 < 150e6 and t1 < 300e6 and t2 < 5e6
+    assert lib.drain_ends(ctypes.c_void_p(out.data_ptr())) == 0
+    assert 125e6 <= int(out[0]) < 300e6

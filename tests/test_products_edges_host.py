@@ -51,3 +51,14 @@ def test_time_in_which_a_kernel_did_not_run_is_not_waited(tmp_path):
     held = [0, 32 * ms, 10 * s, 10 * s + 32 * ms, 10 * s + 64 * ms]
     assert not any(over(held, 2 * s))
     assert over([i * 60 * s for i in range(43)], 2 * s) == [False] * 40 + [True, True]      # and it does end
+
+
+def test_aborted_products_wait_for_what_is_in_flight():
+    # where a wait gives up, the thread that loads drains its loads and the thread that multiplies its products
+    code = _code(os.path.join(CSRC, "tcq_product.cu"))
+    for name, drains in (("pair_kernel(", ("full + 8 * s", "acc_full + 8 *")), ("rows_kernel(", ("full + 8 * s", "acc_full, 0"))):
+        body = code[code.index("    " + name):].split("\n}\n")[0]
+        for what in drains:
+            assert f"mbar_drain({what}" in body, (name, what)
+        # no wait of a thread that issues work is left without a way there
+        assert not re.search(r"mbar_wait\((?:full|empty|acc_empty)[^;{]*\)\) break;", body)

@@ -294,8 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int i = 0; i < kStages; ++i) {
         s = s ? s - 1 : kStages - 1;
         if (s == kStages - 1) ph ^= 1;
-        const unsigned long long t0 = now_ns();
-        while (!mbar_try(full + 8 * s, ph) && now_ns() - t0 < kWaitNs / 16) {}
+        mbar_drain(full + 8 * s, ph);
       }
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
@@ -307,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     while (ok && it.next(p, cluster)) {
       const Job &j = p.job[p.share[it.s].job];
       const int buf = n_acc & 1;
-      if (!mbar_wait(acc_empty + 8 * buf, ((n_acc >> 1) & 1) ^ 1, &stop)) break;
+      if (!mbar_wait(acc_empty + 8 * buf, ((n_acc >> 1) & 1) ^ 1, &stop)) { ok = false; break; }
       tmem_fence_after_sync();
       const uint32_t d = tmem + buf * 256;
       const int w = p.share[it.s].narrow ? 128 : 256;
@@ -331,6 +330,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mma_commit_pair(acc_full + 8 * buf);
       ++n_acc;
     }
+    // gave up: the products issued so far end first (the last commit covers them all)
+    if (!ok && n_acc > 0) mbar_drain(acc_full + 8 * ((n_acc - 1) & 1), ((n_acc - 1) >> 1) & 1);
   } else if (warp >= 2) {
     // ---- results: warp w reads the lanes of quarter w % 4, one half of the columns
     const int quarter = warp & 3, half = (warp - 2) >> 2;
@@ -619,15 +620,15 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
       for (int i = 0; i < Sh::kDepth; ++i) {
         s = s ? s - 1 : Sh::kDepth - 1;
         if (s == Sh::kDepth - 1) ph ^= 1;
-        const unsigned long long t0 = now_ns();
-        while (!mbar_try(full + 8 * s, ph) && now_ns() - t0 < kWaitNs / 16) {}
+        mbar_drain(full + 8 * s, ph);
       }
   } else if (warp == 1 && lane == 0) {
     const uint32_t instr = I8 ? instr_i8(128, NT) : instr_f16(128, NT, p.bf16, 0, 0);
     int s = 0;
     uint32_t ph = 0;
+    bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait(full + 8 * s, ph, &stop)) break;
+      if (!mbar_wait(full + 8 * s, ph, &stop)) { ok = false; break; }
       tmem_fence_after_sync();
       const uint32_t at = ring + s * Sh::kStage;
       const uint64_t w0 = operand_desc(at, false), w1 = operand_desc(at + 16384, false),
@@ -641,6 +642,7 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
       if (++s == Sh::kDepth) { s = 0; ph ^= 1; }
     }
     mma_commit(acc_full);
+    if (!ok) mbar_drain(acc_full, 0);                    // gave up: the products issued so far end first
   } else if (warp >= 2) {
     // sums to shared memory, [column][channel]: the ring is free once all products are done
     const int quarter = warp & 3;

@@ -8,8 +8,8 @@
 // each 64 columns, 8 groups of 1,024 bytes along the contraction.
 //
 // Every wait gives up after two seconds of polling: it raises the block's `stop` flag, at
-// which the block's other waits end too, the copies in flight are waited for,
-// tensor memory is freed and the kernel returns; the library-wide counter
+// which the block's other waits end too, the copies and products in flight are waited
+// for (an eighth of a second at most), tensor memory is freed and the kernel returns; the library-wide counter
 // g_gave_up then says so.
 #pragma once
 
@@ -84,6 +84,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
   *stop = 1u;
   return false;
+}
+
+// After a wait gave up: waits (an eighth of a second at most) for what is still in flight
+// towards `bar`, loads or products, before the block frees its memories and leaves.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  Waited waited(now_ns());
+  while (!mbar_try(bar, parity) && !waited.over(now_ns(), kWaitNs / 16)) {}
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
