@@ -74,7 +74,9 @@ typedef enum tcq_status {
     TCQ_ERR_INVALID_ARG = -1,   /* null pointer, bad size, misalignment, bad enum */
     TCQ_ERR_UNSUPPORTED = -2,   /* valid but not implemented (L, k, V, seq_len, layout) */
     TCQ_ERR_WORKSPACE = -3,     /* workspace pointer missing or smaller than required */
-    TCQ_ERR_CUDA = -4           /* a CUDA call or kernel launch failed */
+    TCQ_ERR_CUDA = -4,          /* a CUDA call or kernel launch failed */
+    TCQ_ERR_TIMEOUT = -5        /* an earlier matrix product on the device gave up a wait
+                                   (tcq_products_gave_up); this call did nothing */
 } tcq_status_t;
 
 /* Bitstream layouts [QTIP, trellis; tail-biting].  Stream bit p of a sequence
@@ -320,6 +322,7 @@ TCQ_API tcq_status_t tcq_rht(const float *W, int64_t rows, int64_t cols, const f
  * overflow).  Any other size is taken; n_in a multiple of
  * 16 bytes (8 elements of 16 bits, 16 of int8) spares a copy of the operands
  * into the workspace, n_out a multiple of 16 elements spares narrow stores.
+ * The first matrix product of a process pins a few words of host memory.
  * Outputs and the workspace may not overlap inputs or one another (an invalid
  * argument).  `ws` is a device workspace of at least the
  * matching *_workspace_size() bytes, 256-byte aligned (a size of 0 allows
@@ -333,9 +336,11 @@ TCQ_API tcq_status_t tcq_rht(const float *W, int64_t rows, int64_t cols, const f
 /* How often a product's kernel gave up waiting for its own loads or products
  * (after two seconds of polling; time in which the kernel did not run hardly
  * counts) on the current device since the library was loaded: 0 unless
- * something is wrong; the outputs of such a call are unspecified.  Waits for
- * the whole device, every stream of it; not allowed while a stream is
- * captured. */
+ * something is wrong.  The outputs of such a call are unspecified; the call
+ * itself has returned long before, so the next matrix product on the device
+ * (tcq_int8_matmul, tcq_gated_ffn, its backward, tcq_int8_gated_ffn) returns
+ * TCQ_ERR_TIMEOUT, once, and does nothing else.  Waits for the whole device,
+ * every stream of it; not allowed while a stream is captured. */
 TCQ_API tcq_status_t tcq_products_gave_up(unsigned int *count);
 
 enum { TCQ_F16 = 0, TCQ_BF16 = 1, TCQ_F32 = 2 };

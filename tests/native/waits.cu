@@ -54,3 +54,17 @@ EXPORT int drain_ends(unsigned long long *out) {
   drain_kernel<<<1, 1>>>(out);
   return (int)cudaDeviceSynchronize();
 }
+
+// A kernel that gave up says so, and what the next call sees: the count, whether there is
+// a note, and whether there still is one.
+__global__ void say_kernel(unsigned int *note) { say_gave_up(note); }
+
+EXPORT int report(unsigned int *count, int *first, int *second) {
+  unsigned int *const note = tcq_host::note_of_device();
+  if (!note || tcq_host::take_note(note)) return -1;
+  say_kernel<<<1, 1>>>(note);
+  if (cudaDeviceSynchronize() != cudaSuccess) return -2;
+  *first = tcq_host::take_note(note);
+  *second = tcq_host::take_note(note);
+  return (int)cudaMemcpyFromSymbol(count, g_gave_up, sizeof(unsigned));
+}

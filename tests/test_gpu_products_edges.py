@@ -74,3 +74,30 @@ def test_a_wait_that_nothing_meets_ends(tcq, tmp_path):
     assert 20e6 <= t0 < 150e6 and t1 < 300e6 and t2 < 5e6
     assert lib.drain_ends(ctypes.c_void_p(out.data_ptr())) == 0
     assert 125e6 <= int(out[0]) < 300e6
+
+
+def test_a_wait_that_ran_out_is_reported_once(tcq, tmp_path):
+    from native import compiled
+    lib = compiled("waits", tmp_path)
+    count, first, second = ctypes.c_uint(), ctypes.c_int(), ctypes.c_int()
+    for i in (1, 2):
+        assert lib.report(ctypes.byref(count), ctypes.byref(first), ctypes.byref(second)) == 0
+        assert (count.value, first.value, second.value) == (i, 1, 0)
+
+
+def test_the_first_product_of_a_process_may_be_a_captured_one(tcq):
+    # its word of host memory is pinned within the call
+    import subprocess
+    import sys
+    code = """
+import torch, trellis_coded_weight_bitshift_b200 as tcq
+x, w = (torch.randn(s, 64, device="cuda").half() for s in (5, 40))
+out, side, graph = torch.empty(5, 40, device="cuda").half(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+side.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+    tcq.gated_ffn(x, w, w, out=out)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, tcq.gated_ffn(x, w, w)) and tcq.products_gave_up() == 0
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)

@@ -5,6 +5,8 @@ import glob
 import os
 import re
 
+from trellis_coded_weight_bitshift_b200 import _abi
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "trellis_coded_weight_bitshift_b200", "csrc")
 
@@ -62,3 +64,13 @@ def test_aborted_products_wait_for_what_is_in_flight():
             assert f"mbar_drain({what}" in body, (name, what)
         # no wait of a thread that issues work is left without a way there
         assert not re.search(r"mbar_wait\((?:full|empty|acc_empty)[^;{]*\)\) break;", body)
+
+
+def test_every_product_asks_whether_an_earlier_one_gave_up():
+    code = _code(os.path.join(CSRC, "tcq_product.cu"))
+    for head in ("static tcq_status_t product(", 'extern "C" tcq_status_t tcq_gated_ffn_backward('):
+        body = code[code.index(head):].split("\n}\n")[0]
+        asks = body.index("if (take_note(note)) return TCQ_ERR_TIMEOUT;")
+        assert asks < body.index("make_copies(") and ".note = note;" in body
+    assert code.count("if (threadIdx.x == 0 && stop) say_gave_up(p.note);") == 2          # both kernels' last words
+    assert "gave up" in _abi.status_string(_abi.TCQ_ERR_TIMEOUT)

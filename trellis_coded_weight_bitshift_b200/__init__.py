@@ -357,7 +357,8 @@ def decode_gemv(bits: torch.Tensor, x: torch.Tensor, rows: int, cols: int, L: in
 
 def products_gave_up() -> int:
     """How often a product's kernel on the current device gave up a wait of
-    its own (0 unless something is wrong); waits for the device."""
+    its own (0 unless something is wrong); waits for the device.  The next
+    product after such a one raises TcqError, with status -5."""
     count = ctypes.c_uint()
     check(lib().tcq_products_gave_up(ctypes.byref(count)), "tcq_products_gave_up")
     return count.value

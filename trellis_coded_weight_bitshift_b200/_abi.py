@@ -12,6 +12,7 @@ TCQ_ERR_INVALID_ARG = -1
 TCQ_ERR_UNSUPPORTED = -2
 TCQ_ERR_WORKSPACE = -3
 TCQ_ERR_CUDA = -4
+TCQ_ERR_TIMEOUT = -5
 
 TAILBITING = 0
 FREE_START = 1

@@ -10,6 +10,7 @@ extern "C" const char *tcq_status_string(tcq_status_t status) {
     case TCQ_ERR_UNSUPPORTED: return "unsupported trellis, layout or size";
     case TCQ_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case TCQ_ERR_CUDA: return "CUDA launch or runtime call failed";
+    case TCQ_ERR_TIMEOUT: return "an earlier product on this device gave up a wait: its outputs are unspecified";
   }
   return "unknown status";
 }

@@ -72,6 +72,7 @@ struct PairParams {
   Share share[5];
   int shares;
   int bf16;
+  unsigned int *note;
   Epilogue e;
 };
 
@@ -420,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
-  if (threadIdx.x == 0 && stop) atomicAdd(&g_gave_up, 1u);
+  if (threadIdx.x == 0 && stop) say_gave_up(p.note);
 }
 
 // ---- few tokens: the weights on the M side
@@ -429,6 +430,7 @@ struct RowsParams {
   int64_t M, N;
   int kb, bf16, wide4;
   void *out;
+  unsigned int *note;
   Epilogue e;
 };
 
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
   __syncwarp();
   if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
   cluster_sync();                                        // no block leaves while its sums are read
-  if (threadIdx.x == 0 && stop) atomicAdd(&g_gave_up, 1u);
+  if (threadIdx.x == 0 && stop) say_gave_up(p.note);
 }
 
 // Rows of `bytes` bytes, packed, to rows `pitch` bytes apart (a multiple of 16);
@@ -1105,6 +1107,8 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
   Workspace w = {(char *)ws};
   PitchCopies copies;
   copies.n = 0;
+  unsigned int *const note = note_of_device();
+  if (take_note(note)) return TCQ_ERR_TIMEOUT;
   Operand A = ready(a, M, K, es, w, copies), B[2];
   for (int i = 0; i < (DUAL ? 2 : 1); ++i) B[i] = ready(i ? w1 : w0, N, K, es, w, copies);
   tcq_status_t st = make_copies(copies, s);
@@ -1120,6 +1124,7 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
     r.bf16 = bf16;
     r.wide4 = N % 4 == 0;
     r.out = out;
+    r.note = note;
     r.e = e;
     return nt == 16   ? launch_rows<I8, DUAL, 16>(r, s)
            : nt == 32 ? launch_rows<I8, DUAL, 32>(r, s)
@@ -1128,6 +1133,7 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
   }
   PairParams p;
   p.bf16 = bf16;
+  p.note = note;
   p.e = e;
   Job &j = p.job[0];
   if (!map_of(&j.a[0], A, 128)) return TCQ_ERR_CUDA;
@@ -1237,6 +1243,8 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
             {{x, 2 * M * K}, {w_gate, 2 * N * K}, {w_up, 2 * N * K}, {gate, 4 * M * N}, {up, 4 * M * N}, {grad_h, 2 * M * N}}))
     return TCQ_ERR_INVALID_ARG;
 
+  unsigned int *const note = note_of_device();
+  if (take_note(note)) return TCQ_ERR_TIMEOUT;
   Workspace w = {(char *)ws};
   const int64_t pitch = round_up(2 * n_out, 16);
   PitchCopies copies;
@@ -1249,6 +1257,7 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
 
   PairParams p;
   p.bf16 = dtype == TCQ_BF16;
+  p.note = note;
   p.e = {dtype, 0, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0};
   int jobs = 0;
   if (grad_x) {

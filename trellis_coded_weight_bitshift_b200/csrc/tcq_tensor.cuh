@@ -13,6 +13,7 @@
 // g_gave_up then says so.
 #pragma once
 
+#include <cstring>
 #include <cuda.h>
 
 #include "tcq_device.cuh"
@@ -204,9 +205,44 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 // for each source file that launches such kernels).
 static __device__ unsigned int g_gave_up;
 
+// A block's last words if one of its waits gave up; `note` is the device's word of host memory.
+__device__ __forceinline__ void say_gave_up(unsigned int *note) {
+  atomicAdd(&g_gave_up, 1u);
+  if (note) {
+    *(volatile unsigned int *)note = 1u;
+    __threadfence_system();
+  }
+}
+
 }  // namespace tcq
 
 namespace tcq_host {
+
+// Words of host memory, one a device, that say_gave_up writes: pinned once a process (in a
+// captured call too, hence the relaxed mode) and kept, as captured graphs refer to them.
+constexpr int kNotes = 64;
+inline unsigned int *notes() {
+  static unsigned int *const p = [] {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    void *q = nullptr;
+    const bool swapped = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+    if (cudaHostAlloc(&q, kNotes * sizeof(unsigned), cudaHostAllocPortable | cudaHostAllocMapped) == cudaSuccess)
+      memset(q, 0, kNotes * sizeof(unsigned));
+    else
+      q = nullptr;
+    if (swapped) cudaThreadExchangeStreamCaptureMode(&mode);
+    return (unsigned int *)q;
+  }();
+  return p;
+}
+// The current device's word (NULL: none), and whether it was written since it was asked last.
+inline unsigned int *note_of_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev < kNotes && notes() ? notes() + dev : nullptr;
+}
+inline bool take_note(unsigned int *note) {
+  return note && __atomic_load_n(note, __ATOMIC_RELAXED) && __atomic_exchange_n(note, 0u, __ATOMIC_ACQUIRE);
+}
 
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
