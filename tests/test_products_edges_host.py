@@ -5,6 +5,11 @@ import glob
 import os
 import re
 
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+import trellis_coded_weight_bitshift_b200 as tcq
 from trellis_coded_weight_bitshift_b200 import _abi
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -74,3 +79,45 @@ def test_every_product_asks_whether_an_earlier_one_gave_up():
         assert asks < body.index("make_copies(") and ".note = note;" in body
     assert code.count("if (threadIdx.x == 0 && stop) say_gave_up(p.note);") == 2          # both kernels' last words
     assert "gave up" in _abi.status_string(_abi.TCQ_ERR_TIMEOUT)
+
+
+# ------------------------------------------------------------------ binding
+
+@pytest.fixture
+def on_host(monkeypatch):
+    """The binding with host tensors for device ones and torch for the launches."""
+    monkeypatch.setattr(tcq, "_require_cuda", lambda *t: None)
+    monkeypatch.setattr(tcq, "_empty", lambda shape, dtype: torch.zeros(shape, dtype=dtype))
+    monkeypatch.setattr(tcq, "_launch_ffn", lambda x, g, u, act, sizes, out, gate, up, ws: out.copy_((x @ g.t()) * (x @ u.t())))
+    monkeypatch.setattr(tcq, "_launch_ffn_backward", lambda x, g, u, gate, up, h, act, sizes, need, ws: tuple(
+        torch.ones_like(t) if n else None for t, n in zip((x, g, u), need)))
+
+
+def _operands():
+    g = torch.Generator().manual_seed(0)
+    return [torch.randn(s, 6, generator=g).half() for s in (3, 5, 5)]
+
+
+@pytest.mark.parametrize("grad_mode", [True, False])
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_tangents_are_refused_not_lost(on_host, grad_mode, which):
+    # the block has no forward-mode rule: a dual operand raises, under no_grad() as well, which leaves forward mode on
+    ops = _operands()
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad_mode):
+        ops[which] = forward_ad.make_dual(ops[which], torch.ones_like(ops[which]))
+        with pytest.raises(RuntimeError, match="jvp"):
+            tcq.GatedFfn.apply(*ops, tcq.ACT_RELU)
+
+
+def test_the_block_saves_only_what_a_backward_pass_needs(on_host):
+    x, g, u = _operands()
+    g.requires_grad_()
+    h = tcq.GatedFfn.apply(x, g, u)
+    assert h.requires_grad and torch.autograd.grad(h.sum(), g)[0].shape == g.shape
+    with torch.no_grad():
+        assert not tcq.GatedFfn.apply(x, g, u).requires_grad
+    assert not tcq.GatedFfn.apply(x, g.detach(), u).requires_grad
+    saved = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: saved.append(t) or t, lambda t: t), torch.no_grad():
+        tcq.GatedFfn.apply(x, g, u)
+    assert not saved

@@ -566,14 +566,13 @@ class GatedFfn(torch.autograd.Function):
 
     @classmethod
     def apply(cls, x, w_gate, w_up, act=ACT_SILU):
-        # inside forward() the grad mode is always off, so it is asked here
-        if not torch.is_grad_enabled():
-            return gated_ffn(x, w_gate, w_up, act)
-        return super().apply(x, w_gate, w_up, act)
+        # inside forward() the grad mode is always off, so it is asked here; without it the call still
+        # goes through the Function, which refuses tangents of forward mode
+        return super().apply(x, w_gate, w_up, act, torch.is_grad_enabled())
 
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, act):
-        if not any(ctx.needs_input_grad[:3]):
+    def forward(ctx, x, w_gate, w_up, act, grad_mode):
+        if not (grad_mode and any(ctx.needs_input_grad[:3])):
             return gated_ffn(x, w_gate, w_up, act)
         sizes = _ffn_operands(x, w_gate, w_up)
         out = _result(None, sizes[:2], x.dtype, x)
@@ -594,7 +593,7 @@ class GatedFfn(torch.autograd.Function):
         _require_cuda(x, grad_out)
         return (*_launch_ffn_backward(x, w_gate, w_up, _ptr(saved), _ptr(saved) + 2 * saved.numel(),
                                       grad_out, ctx.act, ctx.sizes, ctx.needs_input_grad[:3], None),
-                None)
+                None, None)
 
     _once = staticmethod(torch.autograd.function.once_differentiable(_gradients.__func__))
 
