@@ -32,6 +32,7 @@ import ctypes
 from functools import lru_cache
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import _abi
 from ._abi import (ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SILU, FREE_START, OUT_SEQ, OUT_TILE16,
@@ -566,13 +567,15 @@ class GatedFfn(torch.autograd.Function):
 
     @classmethod
     def apply(cls, x, w_gate, w_up, act=ACT_SILU):
-        # inside forward() the grad mode is always off, so it is asked here; without it the call still
-        # goes through the Function, which refuses tangents of forward mode
-        return super().apply(x, w_gate, w_up, act, torch.is_grad_enabled())
+        # inside forward() the grad mode is always off, so it is asked here; a tangent of forward mode,
+        # which no_grad() leaves on, goes to the Function, which refuses it
+        if not torch.is_grad_enabled() and all(unpack_dual(t).tangent is None for t in (x, w_gate, w_up)):
+            return gated_ffn(x, w_gate, w_up, act)
+        return super().apply(x, w_gate, w_up, act)
 
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, act, grad_mode):
-        if not (grad_mode and any(ctx.needs_input_grad[:3])):
+    def forward(ctx, x, w_gate, w_up, act):
+        if not any(ctx.needs_input_grad[:3]):
             return gated_ffn(x, w_gate, w_up, act)
         sizes = _ffn_operands(x, w_gate, w_up)
         out = _result(None, sizes[:2], x.dtype, x)
@@ -593,7 +596,7 @@ class GatedFfn(torch.autograd.Function):
         _require_cuda(x, grad_out)
         return (*_launch_ffn_backward(x, w_gate, w_up, _ptr(saved), _ptr(saved) + 2 * saved.numel(),
                                       grad_out, ctx.act, ctx.sizes, ctx.needs_input_grad[:3], None),
-                None, None)
+                None)
 
     _once = staticmethod(torch.autograd.function.once_differentiable(_gradients.__func__))
 
