@@ -121,3 +121,15 @@ def test_the_block_saves_only_what_a_backward_pass_needs(on_host):
     with torch.autograd.graph.saved_tensors_hooks(lambda t: saved.append(t) or t, lambda t: t), torch.no_grad():
         tcq.GatedFfn.apply(x, g, u)
     assert not saved
+
+
+@pytest.mark.parametrize("which,change", [(0, lambda t: t[:2]), (1, lambda t: t[:, :5].contiguous()), (2, lambda t: t.float()),
+                                          (3, lambda t: t.half()), (3, lambda t: t[:8].clone())])
+def test_the_backward_pass_checks_what_it_is_given_back(on_host, which, change):
+    # the kernels take addresses: a saved tensor that comes back smaller, or of another type, must not reach them
+    count = iter(range(4))
+    leaves = [t.requires_grad_() for t in _operands()]
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (next(count), t), lambda p: change(p[1]) if p[0] == which else p[1]):
+        h = tcq.GatedFfn.apply(*leaves)
+    with pytest.raises(ValueError):
+        h.sum().backward()

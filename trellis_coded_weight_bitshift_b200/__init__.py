@@ -590,10 +590,14 @@ class GatedFfn(torch.autograd.Function):
     @staticmethod
     def _gradients(ctx, grad_out):
         x, w_gate, w_up, saved = ctx.saved_tensors
+        # hooks on saved tensors, or a parameter whose data was exchanged, may bring back others
+        half = (ctx.sizes[0] * ctx.sizes[1] + 3) // 4 * 4
+        if _ffn_operands(x, w_gate, w_up) != ctx.sizes or saved.dtype != torch.float32 or saved.shape != (2 * half,):
+            raise ValueError("the operands of the backward pass are not those of the forward pass")
         grad_out = grad_out.contiguous()
         if grad_out.data_ptr() % 16:                 # a slice of a larger gradient may start anywhere
             grad_out = grad_out.clone()
-        _require_cuda(x, grad_out)
+        _require_cuda(x, saved, grad_out)
         return (*_launch_ffn_backward(x, w_gate, w_up, _ptr(saved), _ptr(saved) + 2 * saved.numel(),
                                       grad_out, ctx.act, ctx.sizes, ctx.needs_input_grad[:3], None),
                 None)
