@@ -101,3 +101,38 @@ torch.cuda.synchronize()
 assert torch.equal(out, tcq.gated_ffn(x, w, w)) and tcq.products_gave_up() == 0
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
+
+
+# ------------------------------------------------------------ pairs of blocks
+
+@pytest.mark.parametrize("M,N,K", [(4096, 8192, 2048), (700, 2500, 264)])
+def test_thousands_of_training_steps(tcq, M, N, K):
+    # the gradients' pairs of blocks start behind the elementwise kernel, whose blocks delay one of the two: every one
+    # of many thousands has to find the other
+    import time
+    g = _gen(3)
+    x, wg, wu = _randn(g, M, K).bfloat16(), _randn(g, N, K).bfloat16() / K ** 0.5, _randn(g, N, K).bfloat16() / K ** 0.5
+    grad = _randn(g, M, N).bfloat16()
+    leaves = [t.requires_grad_() for t in (x, wg, wu)]
+
+    def step():
+        h = tcq.GatedFfn.apply(*leaves, tcq.ACT_GELU)
+        return (h.detach(), *torch.autograd.grad(h, leaves, grad))
+    want = step()
+    side, graph, done = torch.cuda.Stream(), torch.cuda.CUDAGraph(), torch.cuda.Event()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        with torch.cuda.graph(graph, stream=side):
+            for _ in range(10):
+                got = step()
+    torch.cuda.synchronize()
+    for _ in range(10):                                  # a minute's worth of patience for each thousand steps
+        for _ in range(60):
+            graph.replay()
+        done.record()
+        end = time.monotonic() + 60
+        while not done.query():
+            assert time.monotonic() < end, "a step does not end"
+            time.sleep(0.002)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and tcq.products_gave_up() == 0

@@ -133,3 +133,16 @@ def test_the_backward_pass_checks_what_it_is_given_back(on_host, which, change):
         h = tcq.GatedFfn.apply(*leaves)
     with pytest.raises(ValueError):
         h.sum().backward()
+
+
+def test_pair_instructions_run_only_while_both_blocks_are_there():
+    # tensor memory of a pair of blocks is allocated and freed by both: each between two cluster barriers, so that
+    # the other block has started and not left
+    code = _code(os.path.join(CSRC, "tcq_product.cu"))
+    body = code[code.index("    pair_kernel("):].split("\n}\n")[0]
+    marks = [m.group(1) for m in re.finditer(r"\b(cluster_sync|tmem_alloc_pair|tmem_dealloc_pair|mma<I8, true>|mma_commit_pair|"
+                                             r"tma_load_pair|mbar_arrive_at)\(", body)]
+    assert marks[:3] == ["cluster_sync", "tmem_alloc_pair", "cluster_sync"]
+    assert marks[-3:] == ["cluster_sync", "tmem_dealloc_pair", "cluster_sync"] and marks.count("cluster_sync") == 4
+    rows = code[code.index("    rows_kernel("):].split("\n}\n")[0]
+    assert not re.search(r"_pair\(|mma<I8, true>", rows)

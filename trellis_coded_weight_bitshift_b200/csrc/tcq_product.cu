@@ -238,6 +238,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     mbar_init_fence();
   }
+  // An instruction of the pair needs both blocks there, from allocation to release: a block that
+  // allocated before the other had started left that one waiting in its own allocation for good
+  // (one training step in some thousands, behind the elementwise kernel, whose blocks delay one
+  // of the two).
+  __syncwarp();
+  cluster_sync();
   if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), 512);
   tmem_fence_before_sync();
   __syncthreads();
@@ -421,6 +427,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  __syncwarp();
+  cluster_sync();                                        // neither leaves before both have released
   if (threadIdx.x == 0 && stop) say_gave_up(p.note);
 }
 
