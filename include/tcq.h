@@ -346,7 +346,11 @@ TCQ_API tcq_status_t tcq_products_gave_up(unsigned int *count);
 enum { TCQ_F16 = 0, TCQ_BF16 = 1, TCQ_F32 = 2 };
 
 /* Activations: v / (1 + e^-v); v Phi(v) (normal distribution function); its
- * tanh form v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2; max(v, 0). */
+ * tanh form v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2; max(v, 0).
+ * Computed in fp32, each to a relative error of at most (8 + e) 2^-23, where e
+ * is |v| for the first, 3/4 v^2 for the second and 4 sqrt(2/pi) |v + 0.044715
+ * v^3| for the third (the exponential's argument carries its roundings); values
+ * below 2^-110 in size may come out as 0. */
 enum { TCQ_ACT_SILU = 0, TCQ_ACT_GELU = 1, TCQ_ACT_GELU_TANH = 2, TCQ_ACT_RELU = 3 };
 
 /* ------------------------------------------------------------------------

@@ -4,7 +4,7 @@ Bounds.  eps(t) = finfo(t).eps.  Rounding a result to type t costs at most
 eps(t) / 2 of it, or half the smallest subnormal.  A 32-bit sum of n products,
 in any order and with additions that may be truncated instead of rounded
 (2^-23 each), is within (n + 8) 2^-23 of S, the sum of the products'
-magnitudes.  The activations (ex2, rcp and erfc in fp32) are within 2^-19 of
+magnitudes.  The activations (ex2, rcp and a fitted tail in fp32) are within 2^-19 of
 their value plus 2^-19 of their argument's share; their slopes are at most
 1.13 in size and change by at most 1.2 per unit of the argument.
 """

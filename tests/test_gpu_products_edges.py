@@ -1,6 +1,7 @@
 """Edges of the products on decoded weights: the smallest rows, the tails of the
 activations, early starts, reports of waits that ran out."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -136,3 +137,66 @@ def test_thousands_of_training_steps(tcq, M, N, K):
             assert time.monotonic() < end, "a step does not end"
             time.sleep(0.002)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and tcq.products_gave_up() == 0
+
+
+# ------------------------------------------------------------ activations
+
+ACTS = ["silu", "gelu", "gelu_tanh", "relu"]
+
+
+def _act_id(tcq, act):
+    return getattr(tcq, "ACT_" + act.upper())
+
+
+def _activation(v, act):
+    """The activation in 64 bits by functions that keep its tail's digits, and the bound on its fp32 form:
+    (8 + e) 2^-23 of the value, e the weight of the roundings of the exponential's argument: one and a constant's
+    for silu, two and a constant's for gelu, three and a constant's for the tanh form."""
+    z = 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    y, e = {"silu": lambda: (v * torch.sigmoid(v), v.abs()),
+            "gelu": lambda: (v * 0.5 * torch.special.erfc(-v / math.sqrt(2)), 0.75 * v * v),
+            "gelu_tanh": lambda: (v * torch.sigmoid(z), 2 * z.abs()),
+            "relu": lambda: (v.clamp(min=0), torch.zeros_like(v) - 8)}[act]()
+    return y, y.abs() * (8 + e) * 2.0 ** -23 + 2.0 ** -110
+
+
+def _half_step(y, dtype):
+    fi = torch.finfo(dtype)
+    return y.abs() * (fi.eps / 2) + fi.smallest_normal * fi.eps / 2
+
+
+def _within(got, want, bound):
+    off = (got.double() - want).abs() / bound
+    assert float(off.max()) <= 1, (float(off.max()), int(off.argmax()))
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("M,N", [(16001, 3), (16001, 16), (60, 5)])
+def test_activations_keep_their_tails_digits(tcq, act, dtype, M, N):
+    # gates that are exact (multiples of 2^-9 from -15.6 to 15.6) against an up projection of exactly 1, by both kernels
+    n = torch.randint(-8000, 8001, (M,), generator=_gen(M + N), device="cuda") if M < 100 else torch.arange(
+        -8000, 8001, device="cuda")
+    hi = torch.div(n, 64, rounding_mode="floor")
+    a = torch.zeros(M, 16, dtype=torch.int8, device="cuda")
+    a[:, 0], a[:, 1], a[:, 2] = hi, n - 64 * hi, 1
+    wg, wu = torch.zeros(N, 16, dtype=torch.int8, device="cuda"), torch.zeros(N, 16, dtype=torch.int8, device="cuda")
+    wg[:, 0], wg[:, 1], wu[:, 2] = 64, 1, 1
+    one = torch.ones(N, device="cuda")
+    h = tcq.int8_gated_ffn(a, torch.full((M,), 2.0 ** -9, device="cuda"), wg, one, wu, 512 * one, act=_act_id(tcq, act),
+                           out_dtype=dtype)
+    y, bound = _activation(n.double() * 2.0 ** -9, act)
+    y, bound = y[:, None].expand(M, N), bound[:, None].expand(M, N)
+    _within(h, y, bound + y.abs() * 2.0 ** -24 + _half_step(y, dtype) * 1.01)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("M", [4000, 64])
+def test_activations_of_16_bit_projections_keep_their_tails_digits(tcq, act, dtype, M):
+    v = torch.linspace(-8, 8, M, device="cuda").to(dtype)
+    x, one = torch.stack([v, torch.ones_like(v)], 1), torch.tensor([[0, 1]] * 9, dtype=dtype, device="cuda")
+    h, gate, up = tcq.gated_ffn(x, one.flip(1).contiguous(), one, act=_act_id(tcq, act), save=True)
+    assert torch.equal(gate, v.float()[:, None].expand(M, 9)) and bool((up == 1).all())
+    y, bound = _activation(gate.double(), act)
+    _within(h, y, bound + y.abs() * 2.0 ** -24 + _half_step(y, dtype) * 1.01)
