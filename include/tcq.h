@@ -42,7 +42,7 @@
  *     they are ordered on the GPU.
  *   - Arguments are validated on the host before anything is launched; on an
  *     error no work is enqueued and outputs are untouched.  A failed launch
- *     returns TCQ_ERR_CUDA (the CUDA error is left for the caller to query).
+ *     returns TCQ_ERR_CUDA.
  *   - Input values are not checked: non-finite targets give unspecified
  *     outputs.
  */

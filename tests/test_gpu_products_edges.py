@@ -200,3 +200,23 @@ def test_activations_of_16_bit_projections_keep_their_tails_digits(tcq, act, dty
     assert torch.equal(gate, v.float()[:, None].expand(M, 9)) and bool((up == 1).all())
     y, bound = _activation(gate.double(), act)
     _within(h, y, bound + y.abs() * 2.0 ** -24 + _half_step(y, dtype) * 1.01)
+
+
+# ------------------------------------------------------------ errors
+
+def test_a_failed_call_leaves_no_error_behind(tcq):
+    # the count waits for the device, which a captured stream refuses; the next call is not to answer for it
+    bits = torch.zeros(4, 16, dtype=torch.int32, device="cuda").view(torch.uint32)
+    want = tcq.decode(bits, 16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        graph.capture_begin()
+        with pytest.raises(tcq.TcqError):
+            tcq.products_gave_up()
+        with pytest.raises(RuntimeError):
+            graph.capture_end()
+    torch.cuda.synchronize()
+    assert torch.equal(tcq.decode(bits, 16), want)
+    assert tcq.products_gave_up() == 0

@@ -83,6 +83,14 @@ inline bool clash(std::initializer_list<Range> out, std::initializer_list<Range>
   return false;
 }
 
+// A runtime call's status.  The runtime also keeps a failed call's error, which the next
+// launch check of the library would take for its own: it is cleared here.
+inline tcq_status_t status_of(cudaError_t e) {
+  if (e == cudaSuccess) return TCQ_OK;
+  (void)cudaGetLastError();
+  return TCQ_ERR_CUDA;
+}
+
 // cluster: blocks of a cluster along x (0: the kernel's own attribute, or none)
 template <typename... P, typename... A>
 inline tcq_status_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
@@ -100,7 +108,7 @@ inline tcq_status_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, si
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...) == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA;
+  return status_of(cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...));
 }
 
 }  // namespace tcq_host

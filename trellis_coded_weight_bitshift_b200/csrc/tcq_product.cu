@@ -1013,8 +1013,8 @@ void deal(PairParams &p, int jobs, int clusters) {
 
 template <bool I8, bool DUAL>
 tcq_status_t launch_pair(PairParams &p, int jobs, cudaStream_t s) {
-  if (cudaFuncSetAttribute(pair_kernel<I8, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) !=
-      cudaSuccess)
+  if (status_of(cudaFuncSetAttribute(pair_kernel<I8, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kPairSmem)) != TCQ_OK)
     return TCQ_ERR_CUDA;
   deal(p, jobs, clusters_of_gpu());
   int64_t grid = 0;                                      // clusters that get a tile
@@ -1042,8 +1042,8 @@ bool few_tokens(int64_t M) { return M <= (DUAL ? 64 : 256); }
 template <bool I8, bool DUAL, int NT>
 tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
   typedef RowsShape<DUAL, NT> Sh;
-  if (cudaFuncSetAttribute(rows_kernel<I8, DUAL, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
-      cudaSuccess)
+  if (status_of(cudaFuncSetAttribute(rows_kernel<I8, DUAL, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Sh::kSmem)) != TCQ_OK)
     return TCQ_ERR_CUDA;
   // Split the contraction while the clusters still fit the GPU at once (of 148 SMs, 132 hold clusters
   // of four blocks and 120 clusters of eight) and each block keeps four steps of it, eight in a cluster
@@ -1067,8 +1067,8 @@ tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
 extern "C" tcq_status_t tcq_products_gave_up(unsigned int *count) {
   if (!count) return TCQ_ERR_INVALID_ARG;
   // the copy alone would not wait for non-blocking streams
-  if (cudaDeviceSynchronize() != cudaSuccess) return TCQ_ERR_CUDA;
-  return cudaMemcpyFromSymbol(count, g_gave_up, sizeof(unsigned)) == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA;
+  if (status_of(cudaDeviceSynchronize()) != TCQ_OK) return TCQ_ERR_CUDA;
+  return status_of(cudaMemcpyFromSymbol(count, g_gave_up, sizeof(unsigned)));
 }
 
 // What a forward product needs: operands at an aligned pitch, the parts' sums.
@@ -1239,7 +1239,7 @@ extern "C" tcq_status_t tcq_gated_ffn_backward(const void *x, const void *w_gate
   cudaStream_t s = (cudaStream_t)stream;
   if (n_tok == 0) {                                      // no token: the weights' gradients are zero
     for (void *g : {grad_w_gate, grad_w_up})
-      if (g && cudaMemsetAsync(g, 0, (size_t)n_out * n_in * 2, s) != cudaSuccess) return TCQ_ERR_CUDA;
+      if (g && status_of(cudaMemsetAsync(g, 0, (size_t)n_out * n_in * 2, s)) != TCQ_OK) return TCQ_ERR_CUDA;
     return TCQ_OK;
   }
   if (bad_ptr(x) || bad_ptr(w_gate) || bad_ptr(w_up) || bad_ptr(gate) || bad_ptr(up) || bad_ptr(grad_h))

@@ -16,7 +16,7 @@
 #include <cstring>
 #include <cuda.h>
 
-#include "tcq_device.cuh"
+#include "tcq_launch.cuh"
 
 namespace tcq {
 
@@ -225,12 +225,12 @@ inline unsigned int *notes() {
   static unsigned int *const p = [] {
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     void *q = nullptr;
-    const bool swapped = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
-    if (cudaHostAlloc(&q, kNotes * sizeof(unsigned), cudaHostAllocPortable | cudaHostAllocMapped) == cudaSuccess)
+    const bool swapped = status_of(cudaThreadExchangeStreamCaptureMode(&mode)) == TCQ_OK;
+    if (status_of(cudaHostAlloc(&q, kNotes * sizeof(unsigned), cudaHostAllocPortable | cudaHostAllocMapped)) == TCQ_OK)
       memset(q, 0, kNotes * sizeof(unsigned));
     else
       q = nullptr;
-    if (swapped) cudaThreadExchangeStreamCaptureMode(&mode);
+    if (swapped) status_of(cudaThreadExchangeStreamCaptureMode(&mode));
     return (unsigned int *)q;
   }();
   return p;
@@ -238,7 +238,7 @@ inline unsigned int *notes() {
 // The current device's word (NULL: none), and whether it was written since it was asked last.
 inline unsigned int *note_of_device() {
   int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess && dev < kNotes && notes() ? notes() + dev : nullptr;
+  return status_of(cudaGetDevice(&dev)) == TCQ_OK && dev < kNotes && notes() ? notes() + dev : nullptr;
 }
 inline bool take_note(unsigned int *note) {
   return note && __atomic_load_n(note, __ATOMIC_RELAXED) && __atomic_exchange_n(note, 0u, __ATOMIC_ACQUIRE);
@@ -252,7 +252,8 @@ inline EncodeTiled encode_tiled() {
   static const EncodeTiled f = [] {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+    if (status_of(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q)) !=
+            TCQ_OK ||
         q != cudaDriverEntryPointSuccess)
       p = nullptr;
     return (EncodeTiled)p;
