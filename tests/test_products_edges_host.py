@@ -146,3 +146,22 @@ def test_pair_instructions_run_only_while_both_blocks_are_there():
     assert marks[-3:] == ["cluster_sync", "tmem_dealloc_pair", "cluster_sync"] and marks.count("cluster_sync") == 4
     rows = code[code.index("    rows_kernel("):].split("\n}\n")[0]
     assert not re.search(r"_pair\(|mma<I8, true>", rows)
+
+
+def test_rht_keeps_converted_signs_until_the_call(monkeypatch):
+    # signs of another type are converted for the call; both copies have to live until it has been made
+    seen = {}
+
+    class Lib:
+        @staticmethod
+        def tcq_rht(W, R, C, rows, cols, out, stream):
+            for name, at, n in (("rows", rows, R), ("cols", cols, C)):
+                seen[name] = list((ctypes.c_float * n).from_address(at))
+            return 0
+    monkeypatch.setattr(tcq, "lib", lambda: Lib)
+    monkeypatch.setattr(tcq, "_require_cuda", lambda *t: None)
+    monkeypatch.setattr(tcq, "_stream", lambda: 0)
+    for n in (32, 64, 4096):
+        rows, cols = torch.ones(n, dtype=torch.int8), -torch.ones(n, dtype=torch.float64)
+        tcq.rht(torch.zeros(n, n), rows, cols)
+        assert seen["rows"] == [1.0] * n and seen["cols"] == [-1.0] * n

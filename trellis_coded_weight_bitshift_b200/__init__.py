@@ -333,8 +333,9 @@ def rht(W: torch.Tensor, sign_rows: torch.Tensor, sign_cols: torch.Tensor,
     if sign_rows.shape != (R,) or sign_cols.shape != (C,):
         raise ValueError("sign vectors must match W's rows and columns")
     out = torch.empty_like(W) if out is None else _out(out, (R, C), torch.float32, W)
-    check(lib().tcq_rht(_ptr(W), R, C, _ptr(sign_rows.float().contiguous()),
-                        _ptr(sign_cols.float().contiguous()), _ptr(out), _stream()), "tcq_rht")
+    # named: an address does not keep a converted copy alive, and the second could take the first's memory
+    sign_rows, sign_cols = sign_rows.float().contiguous(), sign_cols.float().contiguous()
+    check(lib().tcq_rht(_ptr(W), R, C, _ptr(sign_rows), _ptr(sign_cols), _ptr(out), _stream()), "tcq_rht")
     return out
 
 
