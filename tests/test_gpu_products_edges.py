@@ -6,6 +6,8 @@ import math
 import pytest
 import torch
 
+import test_gpu_products as products
+
 pytestmark = pytest.mark.gpu
 
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
@@ -220,3 +222,106 @@ def test_a_failed_call_leaves_no_error_behind(tcq):
     torch.cuda.synchronize()
     assert torch.equal(tcq.decode(bits, 16), want)
     assert tcq.products_gave_up() == 0
+
+
+# ------------------------------------------------------------ what no test held before
+
+def test_relu_gradients_against_the_formula_and_differences(tcq):
+    # a projection within its bound of zero may take either slope: the output's gradient is zero there, and where the
+    # differences' two points could lie on both sides
+    M, N, K, dtype, step = 40, 72, 48, BF16, 1e-5
+    x, wg, wu, grad = products._ffn_inputs(5, M, N, K, dtype)
+    rg, ru, _, dg, du, _ = products._forward_ref(x, wg, wu, "relu")
+    base = [t.double() for t in (x, wg, wu)]
+    dirs = [_randn(_gen(60 + i), *t.shape).double() for i, t in enumerate(base)]
+    near = dg + 2 * step * (dirs[0].abs() @ base[1].abs().t() + base[0].abs() @ dirs[1].abs().t())
+    grad = torch.where(rg.abs() > near, grad, torch.zeros_like(grad))
+    assert 0 < int((grad != 0).sum()) and int((grad == 0).sum()) < M * N // 50
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu)]
+    grads = torch.autograd.grad(tcq.GatedFfn.apply(*leaves, tcq.ACT_RELU), leaves, grad)
+    ref = products._backward_ref(x, wg, wu, rg, ru, grad, "relu", dtype)
+    # the projections are off by dg and du when the gradients are formed; relu's slope is 0 or 1, and does not change
+    eg, eu = grad.double().abs() * du * 1.01, grad.double().abs() * dg * 1.01
+    more = [eg @ base[1].abs() + eu @ base[2].abs(), eg.t() @ base[0].abs(), eu.t() @ base[0].abs()]
+    for g, (want, bound), m in zip(grads, ref, more):
+        products._within(g, want, bound + m)
+
+    def loss(p):
+        return float(((p[0] @ p[1].t()).clamp(min=0) * (p[0] @ p[2].t()) * grad.double()).sum())
+    for i in range(3):
+        plus, minus = list(base), list(base)
+        plus[i], minus[i] = base[i] + step * dirs[i], base[i] - step * dirs[i]
+        diff = (loss(plus) - loss(minus)) / (2 * step)
+        bound = float(((ref[i][1] + more[i]) * dirs[i].abs()).sum())
+        # the loss is at most quadratic in one operand, so the difference is exact but for 64-bit cancellation
+        assert abs(float((grads[i].double() * dirs[i]).sum()) - diff) <= bound + 1e-6
+
+
+@pytest.mark.parametrize("N,K", [(200, 4096), (77, 8191), (520, 8192), (2048, 2048), (1000, 130)])
+def test_int8_results_do_not_depend_on_the_batch_or_its_split(tcq, N, K):
+    # long sums: split over a cluster, over clusters and joined, or not at all, as the number of tokens decides
+    g = _gen(N + K)
+    a, w, wu = (products._int8(g, m, K) for m in (600, N, N))
+    sa, sw, su, b = (_randn(g, n).exp() * c for n, c in ((600, 1 / 73), (N, 1 / (73 * math.sqrt(K))), (N, 0.01), (N, 1.0)))
+    for dtype in (F32, F16):
+        whole = tcq.int8_matmul(a, sa, w, sw, bias=b, out_dtype=dtype)
+        gated = {act: tcq.int8_gated_ffn(a, sa, w, sw, wu, su, act=_act_id(tcq, act), out_dtype=dtype) for act in ACTS}
+        for lo, hi in ((0, 1), (5, 20), (100, 130), (3, 67), (3, 68), (0, 129), (0, 256), (0, 257), (17, 417)):
+            part, s = a[lo:hi].clone(), sa[lo:hi].clone()
+            assert torch.equal(tcq.int8_matmul(part, s, w, sw, bias=b, out_dtype=dtype), whole[lo:hi]), (lo, hi)
+            for act in ACTS:
+                h = tcq.int8_gated_ffn(part, s, w, sw, wu, su, act=_act_id(tcq, act), out_dtype=dtype)
+                assert torch.equal(h, gated[act][lo:hi]), (lo, hi, act)
+
+
+@pytest.mark.parametrize("shape", [(1,), (7,), (3, 5), (0, 4), (4, 0), (0, 0), (1, 1), (5, 8192)])
+def test_both_ways_to_allocate_give_the_same_tensors(tcq, monkeypatch, shape):
+    for dtype in (torch.int8, torch.uint8, F16, BF16, F32):
+        quick = tcq._empty(shape, dtype)
+        with monkeypatch.context() as m:
+            m.setattr(tcq, "_empty_strided", None)
+            plain = tcq._empty(shape, dtype)
+        for what in ("shape", "dtype", "device", "requires_grad"):
+            assert getattr(quick, what) == getattr(plain, what)
+        assert quick.stride() == plain.stride() and quick.is_contiguous()
+        assert quick.untyped_storage().nbytes() == plain.untyped_storage().nbytes()
+
+
+def test_calls_without_the_quick_allocation(tcq, monkeypatch):
+    x, wg, wu, grad = products._ffn_inputs(3, 20, 72, 41, F16)
+
+    def calls():
+        h, gate, up = tcq.gated_ffn(x, wg, wu, save=True)
+        q, s = tcq.quantize_int8(x)
+        wq, ws = tcq.quantize_int8(wg)
+        return [h, gate, up, q, s, *tcq.gated_ffn_backward(x, wg, wu, gate, up, grad), tcq.int8_matmul(q, s, wq, ws),
+                tcq.int8_gated_ffn(q, s, wq, ws, wq, ws), tcq.gated_ffn(x[:0], wg, wu)]
+    want = calls()
+    monkeypatch.setattr(tcq, "_empty_strided", None)
+    assert all(torch.equal(a, b) for a, b in zip(calls(), want))
+
+
+def test_pairs_of_blocks_start_behind_anything(tcq):
+    # products of pairs, products of clusters, elementwise kernels and the gradients' chain on four streams at once
+    import time
+    a = products._ffn_inputs(1, 1500, 2048, 512, BF16)
+    b = products._ffn_inputs(2, 40, 2048, 512, F16)
+    c = products._ffn_inputs(3, 300, 1000, 130, BF16)
+    _, gate, up = tcq.gated_ffn(*c[:3], save=True)
+    z = torch.zeros(1 << 22, device="cuda")
+    work = [lambda: (tcq.gated_ffn(*a[:3]),), lambda: (tcq.gated_ffn(*b[:3]),), lambda: (z.mul_(1.0),),
+            lambda: tcq.gated_ffn_backward(*c[:3], gate, up, c[3])]
+    want = [w() for w in work]
+    streams, done = [torch.cuda.Stream() for _ in work], [torch.cuda.Event() for _ in work]
+    torch.cuda.synchronize()
+    got = [None] * len(work)
+    for _ in range(2000):
+        for i, (stream, call) in enumerate(zip(streams, work)):
+            with torch.cuda.stream(stream):
+                got[i] = call()
+                done[i].record()
+    end = time.monotonic() + 60
+    while not all(e.query() for e in done):
+        assert time.monotonic() < end, "a call does not end"
+        time.sleep(0.002)
+    assert all(torch.equal(p, q) for g, w in zip(got, want) for p, q in zip(g, w)) and tcq.products_gave_up() == 0
