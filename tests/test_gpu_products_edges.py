@@ -325,3 +325,23 @@ def test_pairs_of_blocks_start_behind_anything(tcq):
         assert time.monotonic() < end, "a call does not end"
         time.sleep(0.002)
     assert all(torch.equal(p, q) for g, w in zip(got, want) for p, q in zip(g, w)) and tcq.products_gave_up() == 0
+
+
+@pytest.mark.parametrize("N", [40, 4096, 4097])
+@pytest.mark.parametrize("K", [512, 513, 1536, 1537])
+def test_int8_results_on_both_sides_of_the_kernels_borders(tcq, N, K):
+    # up to 32 tokens one kernel works, beyond them sums, channels and tokens decide
+    g = _gen(N + K)
+    a, w, wu = (products._int8(g, m, K) for m in (257, N, N))
+    sa, sw, su = (_randn(g, n).exp() * c for n, c in ((257, 1 / 73), (N, 1 / (73 * math.sqrt(K))), (N, 0.01)))
+
+    def both(lo, hi):
+        part, s = a[lo:hi].clone(), sa[lo:hi].clone()
+        return torch.cat([tcq.int8_matmul(part, s, w, sw, out_dtype=F32),
+                          tcq.int8_gated_ffn(part, s, w, sw, wu, su, out_dtype=F32)], 1)
+    want = torch.cat([both(i, min(i + 32, 257)) for i in range(0, 257, 32)])
+    p = (a.double() @ w.double().t()) * sa.double()[:, None] * sw.double()
+    products._within(want[:, :N], p, p.abs() * 4.01 * 2.0 ** -24)
+    for M in (33, 64, 65, 128, 129, 256, 257):
+        assert torch.equal(both(0, M), want[:M]), M
+        assert torch.equal(both(257 - M, 257), want[257 - M:]), M

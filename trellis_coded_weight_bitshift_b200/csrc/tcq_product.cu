@@ -937,7 +937,9 @@ int clusters_of_gpu() { return std::max(1, sm_count() / 2); }
 // Parts of the contraction for `count` tiles of `steps` steps whose sums are `sums`
 // bytes: the number, of those that the clusters hold at once with eight steps or
 // more each, that takes the least time by what was measured: 0.26 us a step while
-// few clusters run, 3 us to join and the parts' sums twice through L2 at 6 TB/s.
+// few clusters run, 3 us to join and the parts' sums twice through L2 at 6 TB/s.  Less
+// than 15% to be had by that is none in fact, as the steps of a wide product take longer
+// (int8 192 x 8192 x 8192, 32 tiles: whole 24.6, in two parts 29.3, by the formula 15.5 of 16.6).
 // Measured (us, whole / best split): int8 512 x 8192 x 1024 25.8 / 16.9 (four
 // parts), 1024 tokens 26.7 / 19.6 (four); 512 x 8192 x 2048 26.8 / 19.9 (four); int8
 // gated block 129 x 8192 x 2048 26.4 / 19.5 (four); not split 512 x 2048 x 2048 11.1 /
@@ -945,7 +947,7 @@ int clusters_of_gpu() { return std::max(1, sm_count() / 2); }
 int parts_of(int64_t count, int64_t steps, double sums) {
   const int64_t most = std::min<int64_t>(clusters_of_gpu() / std::max<int64_t>(1, count), steps / 8);
   int best = 1;
-  double least = 0.26 * (double)steps;
+  double least = 0.85 * 0.26 * (double)steps;
   for (int64_t s = 2; s <= most; ++s) {
     const double t = 0.26 * (double)steps / (double)s + 3.0 + 2.0 * (double)s * sums / 6e6;
     if (t < least) {
@@ -1030,14 +1032,26 @@ tcq_status_t launch_pair(PairParams &p, int jobs, cudaStream_t s) {
   return st;
 }
 
-// Which kernel: up to 64 tokens (256 of a single product) rows_kernel.  Measured,
-// us, rows / pair: int8 8192 x 8192 at 64 tokens 16.4 / 23.0, 128 19.7 / 27.7, 192
-// 27.5 / 30.4, 256 28.4 / 26.1, 384 43.2 / 33.9; 8192 -> 1024 at 256 11.6 / 14.0; 2048
-// x 2048 at 256 8.4 / 9.2; bf16 gated block 2048 -> 8192 at 64 17.3 / 19.7, 96 19.3 /
-// 20.2, 128 21.0 / 20.6, 1024 -> 2736 at 96 9.3 / 9.1; int8 gated block 2048 -> 8192
-// at 48 12.0 / 14.6, 64 13.3 / 13.0.
+// Which kernel.  rows_kernel reads the weights once for each tile of tokens and then finishes
+// 128 channels by its tile of tokens in each cluster: best for long sums of few tokens.  Of a
+// short sum the finishing is most of it, and with two tiles of tokens and many channels the
+// pairs' tiles fill the GPU and read less.  Measured, us, rows / pair, steps of 128 bytes of the
+// contraction:
+//   to 32 tokens: rows (20 tokens, 1024 channels, 4 steps, two projections 7.2 / 6.1 is its worst);
+//   to 64, 4 steps: 9.2 / 6.0 (512 and 2048 channels), 9.4 / 7.0 (8192), two projections 11.4 / 6.1
+//     (1024), 9.1 / 8.6 (8192, 16 bits; 40 tokens 7.5 / 8.5); 8 steps: 7.0 / 7.0 and 7.7 / 8.4, two projections 9.2 / 7.2
+//     and 10.2 / 10.4, 16 bits 7.7 / 7.1 and 8.9 / 10.2; 16 steps of two, 8192: 13.2 / 13.6;
+//   two projections of 96 tokens, bf16, 2048 -> 8192: 19.3 / 20.2, 128: 21.0 / 20.6, 1024 -> 2736 at 96
+//     9.3 / 9.1;
+//   to 128, one projection, 4 steps: 14.4 / 6.3, 8: 10.1 / 7.3, 12: 10.6 / 8.5, 64 (8192) 19.7 / 27.7;
+//   to 256, 12 steps: 10.6 / 8.5; 16: 8.2 / 9.5 (2048), 10.0 / 9.6 (4096), 13.5 / 10.7 (8192); 32: 9.2 /
+//     13.3, 11.7 / 14.2, 18.1 / 15.4; 64: 12.5 / 17.4, 15.8 / 20.4, 27.0 / 24.6.
 template <bool DUAL>
-bool few_tokens(int64_t M) { return M <= (DUAL ? 64 : 256); }
+bool few_tokens(int64_t M, int64_t N, int64_t steps) {
+  if (M <= 32) return true;
+  if (M <= 64) return steps > 4 || (DUAL && M <= 48 && N > 4096);
+  return !DUAL && steps > 12 && (M <= 128 || (M <= 256 && N <= 4096));
+}
 
 template <bool I8, bool DUAL, int NT>
 tcq_status_t launch_rows(const RowsParams &p, cudaStream_t s) {
@@ -1075,7 +1089,7 @@ extern "C" tcq_status_t tcq_products_gave_up(unsigned int *count) {
 template <bool DUAL>
 static size_t product_bytes(int64_t M, int64_t N, int64_t K, int es) {
   return pitch_bytes(M, K * es) + (DUAL ? 2 : 1) * pitch_bytes(N, K * es) +
-         (few_tokens<DUAL>(M) ? 0 : plan_of(M, N, DUAL ? 128 : 256, 1, DUAL ? 2 : 1, tiles(K * es, 128)).bytes);
+         (few_tokens<DUAL>(M, N, tiles(K * es, 128)) ? 0 : plan_of(M, N, DUAL ? 128 : 256, 1, DUAL ? 2 : 1, tiles(K * es, 128)).bytes);
 }
 
 extern "C" size_t tcq_int8_matmul_workspace_size(int64_t n_tok, int64_t n_out, int64_t n_in) {
@@ -1121,7 +1135,7 @@ static tcq_status_t product(const void *a, const void *w0, const void *w1, int e
   for (int i = 0; i < (DUAL ? 2 : 1); ++i) B[i] = ready(i ? w1 : w0, N, K, es, w, copies);
   tcq_status_t st = make_copies(copies, s);
   if (st != TCQ_OK) return st;
-  if (few_tokens<DUAL>(M)) {
+  if (few_tokens<DUAL>(M, N, tiles(K * es, 128))) {
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     RowsParams r;
     if (!map_of(&r.w[0], B[0], 128) || (DUAL && !map_of(&r.w[1], B[1], 128)) || !map_of(&r.x, A, nt))
