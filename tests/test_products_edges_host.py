@@ -165,3 +165,11 @@ def test_rht_keeps_converted_signs_until_the_call(monkeypatch):
         rows, cols = torch.ones(n, dtype=torch.int8), -torch.ones(n, dtype=torch.float64)
         tcq.rht(torch.zeros(n, n), rows, cols)
         assert seen["rows"] == [1.0] * n and seen["cols"] == [-1.0] * n
+
+
+def test_loads_behind_an_early_start_are_fenced():
+    # tensor-map loads read what earlier kernels stored: behind the wait, and behind a fence between the two paths
+    code = _code(os.path.join(CSRC, "tcq_product.cu"))
+    for name, first in (("    pair_kernel(", "tma_load_pair("), ("    rows_kernel(", "load(kb0 + i, i)")):
+        body = code[code.index(name):].split("\n}\n")[0]
+        assert body.index("after_previous()") < body.index("fence_before_loads()") < body.index(first)

@@ -255,6 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (warp == 0 && lane == 0) {
     // ---- loads: this block's rows of A and half of B, counted by the first block's barrier
+    fence_before_loads();
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -595,8 +596,10 @@ __global__ void __launch_bounds__(192, RowsShape<DUAL, NT>::kBlocksPerSm)
     if (DUAL) tma_load(at + 16384, &p.w[1], k, (int)n0, bar);
     tma_load(at + Sh::kWeightBytes, &p.x, k, (int)m0, bar);
   };
-  if (threadIdx.x == 0)
+  if (threadIdx.x == 0) {
+    fence_before_loads();
     for (int i = 0; i < ahead; ++i) load(kb0 + i, i);
+  }
   // the scales of this thread's first results, while the operands stream
   const int quads = 32 / split, cols = (int)min((int64_t)NT, p.M - m0);
   float sa0 = 0.0f, s00[4] = {}, s10[4] = {};

@@ -116,6 +116,11 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// Before a thread's first tensor-map loads: what earlier kernels wrote by ordinary stores
+// (copies, dg and du) reaches them through another path, also where this kernel started
+// before those had ended.
+__device__ __forceinline__ void fence_before_loads() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // A tile of one block's operand; `bar` may be the cluster's first block's.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
   asm volatile(
