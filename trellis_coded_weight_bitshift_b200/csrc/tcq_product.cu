@@ -15,8 +15,8 @@
 // 16-bit step (8 MFLOP), which neither the shared-memory port (64 of 128 bytes a
 // clock) nor L2 limits; a 128 x 128 tile of one block would need all of the port.
 //
-// Measured (steady loop): int8 3001 x 8192 x 8192 153 us (2.6 POP/s), gated block
-// 3001 x 2048 x 8192 bf16 155 us (1.30 PFLOP/s; the library's product of the same
+// Measured (steady loop): int8 3001 x 8192 x 8192 151 us (2.66 POP/s), gated block
+// 3001 x 2048 x 8192 bf16 152 us (1.33 PFLOP/s; the library's product of the same
 // projections without the gate 162), the three gradients of 4096 x 2048 x 8192 374 us
 // (1.47 PFLOP/s).  The tensor pipe is busy 89 to 95% of the active cycles (70% where a
 // tile has only 16 steps) and the clock falls to 1.5 to 1.65 GHz: power bounds them.
@@ -795,8 +795,10 @@ template <> __device__ __forceinline__ __half narrow<__half>(float v) { return _
 template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 // dg = grad u act'(g), du = grad act(g), in rows `pitch` elements apart; eight
-// values a thread where rows start on 16-byte boundaries (N = 8), else one.  Bound by
-// HBM: 4096 x 8192 bf16, 470 MB in 65 us (7.2 TB/s).
+// values a thread where rows start on 16-byte boundaries (N = 8), else one.  Both are rounded to
+// 16 bits, as they are operands of a 16-bit product: with that a gradient's error is sqrt 2 of its
+// last rounding's (0.0023 against 0.0017 in bf16); kept as two 16-bit parts each they would double
+// the products.  Bound by HBM: 4096 x 8192 bf16, 470 MB in 65 us (7.2 TB/s).
 template <typename T, int N>
 __global__ void __launch_bounds__(256) gate_grad_kernel(const T *grad, const float *gate,
                                                         const float *up, int64_t rows, int64_t cols,
@@ -920,8 +922,8 @@ bool map_of(CUtensorMap *m, const Operand &o, int box_rows) {
 // Row tiles of a band: the second operand is read from memory once for each
 // band, so bands are as tall as leaves the first operand's rows (32 KB a step and
 // tile) within 24 MB of the 126 MB L2, at least 8, and of equal height (gated block
-// 3001 x 2048 x 8192: 168.5 us in bands of 8, 164.9 in one of 12; int8 3001 x 8192 x
-// 8192 165.3 and 162.0).
+// 3001 x 2048 x 8192: 155.0 us in bands of 8, 151.7 in one of 12; int8 3001 x 8192 x
+// 8192 153.5 and 149.6).
 int band_of(const Job &j) {
   const int64_t most = std::max<int64_t>(8, (24 << 20) / (32768ll * j.kb * j.segs));
   return (int)tiles(j.mt, tiles(j.mt, most));
@@ -931,10 +933,12 @@ int band_of(const Job &j) {
 // tiles goes first; clusters that its last round leaves idle take as many of the
 // other's tiles as that round lasts; then the rest goes round.  What is left of
 // the last round, if it occupies at most half of the clusters, is dealt in half
-// tiles.  Measured: gradients of 4096 x 2048 x 8192 447 us for all three in one
-// launch (elementwise pass counted), grad_x alone 300, the weights' two alone 288;
-// gated block 3001 x 2048 x 8192 (768 tiles, 74 clusters) 169.6 us in whole tiles,
-// 168.9 with the last 28 halved (power, not the idle SMs, sets the time there).
+// tiles.  Measured: gradients of 4096 x 2048 x 8192 446 us for all three in one
+// launch (elementwise pass counted), grad_x alone 272, the weights' two alone 280.
+// Half tiles: int8 256 x 512 -> 2048 7.7 -> 6.3 us, gated block 100 x 1024 -> 2048
+// 10.9 -> 9.2, 1024 x 1024 -> 8192 33.6 -> 32.1, training step 512 x 1024 x 2048 41.9
+// -> 37.9; at 3001 x 2048 x 8192 (768 tiles, 74 clusters) nothing (power, not the
+// idle SMs, sets the time there).
 int clusters_of_gpu() { return std::max(1, sm_count() / 2); }
 
 // Parts of the contraction for `count` tiles of `steps` steps whose sums are `sums`
